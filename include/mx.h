@@ -463,6 +463,107 @@ mx_status mx_moe_combine_peer(const void *const *y_peers, int32_t ranks, int64_t
                               const int32_t *src_rank, const int32_t *src_row, const float *w, int64_t tokens,
                               int32_t topk, void *out_bf16, int32_t *dev_status, mx_stream_t stream);
 
+/* ------------------------------------------------------------------ 16-bit products
+ *
+ * What a mixture-of-experts training step keeps out of FP8: the dense layers
+ * around the experts, experts held in 16 bits, and the optimiser's update of
+ * their weights (the pages quantise the expert GEMMs; "DeepSeek drops DeepGEMM"
+ * page, FP8 mixed precision: sensitive parts stay in BF16).  Operands are BF16
+ * or FP16, row-major, 16-byte aligned; sums are FP32; results are rounded once.
+ * Row lengths that a tensor map must describe are multiples of 8 elements.
+ */
+typedef enum mx_dtype { MX_BF16 = 0, MX_FP16 = 1, MX_FP32 = 2 } mx_dtype;
+
+/* act(z): z; max(z, 0); z / (1 + e^-z); z Phi(z) (Phi the normal distribution
+ * function); z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum mx_activation {
+    MX_ACT_NONE = 0,
+    MX_ACT_RELU = 1,
+    MX_ACT_SILU = 2,
+    MX_ACT_GELU = 3,
+    MX_ACT_GELU_TANH = 4
+} mx_activation;
+
+/*
+ * Linear layer with bias, activation and residual in the GEMM's epilogue:
+ *   z = x w^T + bias;   y = act(z) + residual
+ *   x [m, k], w [n, k], bias [n] (nullable), residual [m, n] (nullable), all of
+ *   `dtype` (MX_BF16 or MX_FP16); y [m, n] out; z [m, n] out (nullable): the
+ *   pre-activation, for mx_linear_act_backward.  y is computed from the FP32 z.
+ *   y may be the residual itself; outputs overlap nothing else.
+ * Requires k > 0, k % 8 == 0, n % 8 == 0, sizes at most 2^31 - 1024.
+ * m == 0 or n == 0 is a no-op.
+ */
+mx_status mx_linear_act(const void *x, const void *w, const void *bias, const void *residual, void *z, void *y,
+                        int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act, int32_t *dev_status,
+                        mx_stream_t stream);
+
+/*
+ * Its backward pass, from dy = dL/dy [m, n] and the z that the forward pass kept:
+ *   dz = dy * act'(z);   dx = dz w;   dw = dz^T x;   dbias[j] = sum_i dz[i, j]
+ * (the residual's gradient is dy).  dx [m, k], dw [n, k] and dbias [n] are each
+ * nullable: not wanted.  With an activation, z and dz [m, n] (out; rounded to
+ * `dtype` for the two products) are needed; without one both may be NULL and dy
+ * takes dz's place.  dbias sums the unrounded products in FP32 in a fixed order;
+ * it needs `workspace` of mx_linear_act_backward_workspace_bytes(m, n) bytes.
+ * ReLU's derivative at zero is 0.  x is read for dw only, w for dx only (NULL
+ * otherwise).  m == 0 gives zero dw and dbias; n == 0 gives zero dx.
+ */
+size_t mx_linear_act_backward_workspace_bytes(int64_t m, int64_t n);
+mx_status mx_linear_act_backward(const void *dy, const void *z, const void *x, const void *w, void *dz, void *dx,
+                                 void *dw, void *dbias, int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act,
+                                 void *workspace, size_t workspace_bytes, int32_t *dev_status, mx_stream_t stream);
+
+/*
+ * 16-bit products grouped by expert, over ragged groups: expert e owns rows
+ * [group_offsets[e], group_offsets[e+1]) (DEVICE int32[groups + 1], any
+ * non-decreasing values in [0, m_total]; mx_moe_route with pad = 1 makes them,
+ * or the padded ones of mx_grouped_gemm_contiguous).
+ *   forward   d[i, :] = a[i, :] b[e]^T          a [m_total, k], b [groups, n, k], d [m_total, n]
+ *   dgrad     da[i, :] = dd[i, :] b[e]          dd [m_total, n], da [m_total, k]
+ *   wgrad     db[e] = sum_i dd[i, :]^T a[i, :]  db [groups, n, k]
+ * Rows before the first offset and at or behind the last are left untouched
+ * (forward, dgrad) and add nothing (wgrad); an expert without rows gets a zero
+ * db.  What the rows outside a group hold, infinities and NaN included, does not
+ * reach it.  wgrad's result is `dtype` or MX_FP32 (out_dtype).  Requires k and
+ * n positive multiples of 8, groups <= 1024, m_total <= 2^31 - 1024.
+ * m_total == 0 is a no-op (wgrad: zeros).  Offsets out of order or range set
+ * MX_DEV_BAD_OFFSETS and nothing is written.
+ */
+mx_status mx_grouped_gemm_ragged(const void *a, const void *b, const int32_t *group_offsets, int32_t groups,
+                                 int64_t m_total, int64_t n, int64_t k, int32_t dtype, void *d, int32_t *dev_status,
+                                 mx_stream_t stream);
+mx_status mx_grouped_gemm_ragged_dgrad(const void *dd, const void *b, const int32_t *group_offsets, int32_t groups,
+                                       int64_t m_total, int64_t n, int64_t k, int32_t dtype, void *da,
+                                       int32_t *dev_status, mx_stream_t stream);
+mx_status mx_grouped_gemm_ragged_wgrad(const void *dd, const void *a, const int32_t *group_offsets, int32_t groups,
+                                       int64_t m_total, int64_t n, int64_t k, int32_t dtype, int32_t out_dtype,
+                                       void *db, int32_t *dev_status, mx_stream_t stream);
+
+/*
+ * Orthogonalisation of a batch of weight updates by Newton-Schulz products (the
+ * step of the Muon optimiser that replaces a momentum by a nearly orthogonal
+ * matrix with the same singular vectors):
+ *   X = G / (|G|_F + eps); then, `steps` times with (a, b, c) = coeffs[3 i ..]:
+ *   A = X X^T;  X = a X + (b A + c A^2) X        (X^T X for more rows than columns)
+ *   g [batch, m, n], MX_BF16 or MX_FP32 (g_dtype); out [batch, m, n] BF16; coeffs
+ *   a HOST array of 3 * steps floats, read during the call.
+ * Products are of FP16 numbers scaled by powers of two, with FP32 sums.  The
+ * coefficients must keep the singular values, which start in [0, 1], at most
+ * 3.9, and |b s^2 + c s^4| and |a + b s^2 + c s^4| at most 15.5 on the way (FP16's
+ * range; the usual (3.4445, -4.775, 2.0315) stays below 1.3 and 3.5), else
+ * MX_ERR_INVALID_ARGUMENT.  A matrix with a NaN or an infinity gives NaN (that
+ * matrix only); a zero matrix gives zeros.  m, n in [1, 2^20], any values;
+ * batch <= 65535; 1 <= steps <= 16; eps >= 0.  out may be g where g is BF16.
+ * workspace: mx_orthogonalize_workspace_bytes(...) bytes, 256-byte aligned,
+ * written by the call; calls that may run at the same time need one each.
+ * batch, m or n == 0 is a no-op.
+ */
+size_t mx_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int32_t g_dtype, int32_t steps);
+mx_status mx_orthogonalize(const void *g, int32_t g_dtype, void *out_bf16, int64_t batch, int64_t m, int64_t n,
+                           int32_t steps, const float *coeffs, float eps, void *workspace, size_t workspace_bytes,
+                           int32_t *dev_status, mx_stream_t stream);
+
 /* Failure detection (no counterpart on the pages; a property of this
  * implementation).  Every wait inside the GEMM kernels (a pipeline stage
  * landing, an accumulator being drained, ...) is bounded: a wait that runs

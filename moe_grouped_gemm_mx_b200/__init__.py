@@ -13,9 +13,13 @@ Function names match the C ABI:
     d     = mx_gemm(qa, sfa, qb, sfb)                   # D = A B^T, bf16 [M, N]
     d     = mx_grouped_gemm_contiguous(qa, sfa, qb, sfb, group_offsets)
     d     = mx_grouped_gemm_masked(qa, sfa, qb, sfb, masked_m)
+    y     = mx_linear_act(x, w, bias, residual, "gelu") # 16-bit operands, epilogue fused
+    d     = mx_grouped_gemm_ragged(a, b, group_offsets) # 16-bit operands, groups of any size
+    u     = mx_orthogonalize(momentum)                  # Newton-Schulz, batched
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -30,6 +34,9 @@ __all__ = [
     "mx_quantize_bf16_to_e4m3_block128x128", "mx_gemm_tilewise", "mx_grouped_gemm_contiguous_tilewise",
     "mx_moe_max_rows", "mx_moe_route", "mx_moe_dispatch_quant", "mx_moe_scatter_rows", "mx_gather_rows",
     "mx_moe_combine", "mx_moe_peer_plan", "mx_moe_dispatch_quant_peer", "mx_moe_combine_peer",
+    "mx_linear_act", "mx_linear_act_backward", "mx_linear_act_backward_workspace_bytes", "mx_grouped_gemm_ragged",
+    "mx_grouped_gemm_ragged_dgrad", "mx_grouped_gemm_ragged_wgrad", "mx_orthogonalize",
+    "mx_orthogonalize_workspace_bytes", "ACTIVATIONS",
     "read_internal_status", "MX_DEV_BAD_OFFSETS", "MX_DEV_BAD_MASK", "MX_DEV_TIMEOUT", "MX_DEV_BAD_INDEX",
     "C_SYMBOLS",
 ]
@@ -55,9 +62,15 @@ C_SYMBOLS = [
     "mx_moe_max_rows", "mx_moe_route", "mx_moe_dispatch_quant", "mx_moe_scatter_rows", "mx_gather_rows",
     "mx_moe_combine", "mx_moe_peer_plan", "mx_moe_dispatch_quant_peer", "mx_moe_combine_peer",
     "mx_set_wait_limit_ns", "mx_wait_limit_ns", "mx_gemm_batch",
+    "mx_linear_act", "mx_linear_act_backward", "mx_linear_act_backward_workspace_bytes", "mx_grouped_gemm_ragged",
+    "mx_grouped_gemm_ragged_dgrad", "mx_grouped_gemm_ragged_wgrad", "mx_orthogonalize",
+    "mx_orthogonalize_workspace_bytes",
 ]
 
 MX_GEMM_BATCH_MAX = 4
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # mx_dtype
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # mx_activation
 
 
 class _QuantJob(ctypes.Structure):
@@ -146,6 +159,24 @@ def _load():
     L.mx_set_wait_limit_ns.restype = ctypes.c_int
     L.mx_wait_limit_ns.argtypes = []
     L.mx_wait_limit_ns.restype = ctypes.c_uint64
+    SZ = ctypes.c_size_t
+    L.mx_linear_act.argtypes = [P, P, P, P, P, P, I64, I64, I64, I32, I32, P, P]
+    L.mx_linear_act.restype = ctypes.c_int
+    L.mx_linear_act_backward_workspace_bytes.argtypes = [I64, I64]
+    L.mx_linear_act_backward_workspace_bytes.restype = SZ
+    L.mx_linear_act_backward.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, P, SZ, P, P]
+    L.mx_linear_act_backward.restype = ctypes.c_int
+    L.mx_grouped_gemm_ragged.argtypes = [P, P, P, I32, I64, I64, I64, I32, P, P, P]
+    L.mx_grouped_gemm_ragged.restype = ctypes.c_int
+    L.mx_grouped_gemm_ragged_dgrad.argtypes = [P, P, P, I32, I64, I64, I64, I32, P, P, P]
+    L.mx_grouped_gemm_ragged_dgrad.restype = ctypes.c_int
+    L.mx_grouped_gemm_ragged_wgrad.argtypes = [P, P, P, I32, I64, I64, I64, I32, I32, P, P, P]
+    L.mx_grouped_gemm_ragged_wgrad.restype = ctypes.c_int
+    L.mx_orthogonalize_workspace_bytes.argtypes = [I64, I64, I64, I32, I32]
+    L.mx_orthogonalize_workspace_bytes.restype = SZ
+    L.mx_orthogonalize.argtypes = [P, I32, P, I64, I64, I64, I32, ctypes.POINTER(ctypes.c_float), ctypes.c_float, P,
+                                   SZ, P, P]
+    L.mx_orthogonalize.restype = ctypes.c_int
     return L
 
 
@@ -743,6 +774,263 @@ def mx_moe_combine_peer(y_ptrs: torch.Tensor, y_rows: int, n: int, src_rank: tor
     _raise(_lib.mx_moe_combine_peer(_ptr_table(y_ptrs, ranks, "y_ptrs"), ranks, y_rows, n, _ptr(src_rank),
                                     _ptr(src_row), _ptr(w), tokens, topk, _ptr(out), _ptr(dev_status),
                                     _stream(stream)), "mx_moe_combine_peer")
+    return out
+
+
+# ---------------------------------------------------------------- 16-bit products
+
+@contextlib.contextmanager
+def _launch_on(t: torch.Tensor, stream):
+    """The device of ``t`` and the stream the call runs on, both made current,
+    so that what the call allocates belongs to that stream."""
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device)
+        if s.device != t.device:
+            raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
+        with torch.cuda.stream(s):
+            yield s.cuda_stream
+
+
+def _check16(t: torch.Tensor, name: str, shape, dtype, device):
+    """A contiguous tensor of the given shape and type on the given device."""
+    _check(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+
+
+def _operand16(t: torch.Tensor, name: str, dims: int) -> torch.dtype:
+    """The type of the operand that sets the call's type (BF16 or FP16)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    _check(t, t.dtype, name)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {dims}-D")
+    return t.dtype
+
+
+def _status_on(dev_status, device):
+    if dev_status is not None and isinstance(dev_status, torch.Tensor) and dev_status.device != device:
+        raise ValueError(f"dev_status is on {dev_status.device}, the tensors on {device}")
+    return _status_arg(dev_status)
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def mx_linear_act(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+                  residual: torch.Tensor | None = None, activation: str = "none", return_z: bool = False,
+                  z: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                  dev_status: torch.Tensor | None = None, stream=None):
+    """y = act(x w^T + bias) + residual on BF16 or FP16 tensors: x [M, K],
+    w [N, K], bias [N], residual [M, N] -> y [M, N].  With ``return_z`` (or an
+    output ``z``) also the pre-activation z [M, N]: returns (y, z).  ``y`` may
+    be ``residual``."""
+    dt = _operand16(x, "x", 2)
+    act = _activation(activation)
+    m, k = x.shape
+    _operand16(w, "w", 2)
+    n = w.shape[0]
+    dev = x.device
+    _check16(w, "w", (n, k), dt, dev)
+    with _launch_on(x, stream) as s:
+        y = torch.empty((m, n), dtype=dt, device=dev) if y is None else y
+        if return_z and z is None:
+            z = torch.empty((m, n), dtype=dt, device=dev)
+        for t, nm, shape in ((bias, "bias", (n,)), (residual, "residual", (m, n)), (z, "z", (m, n)), (y, "y", (m, n))):
+            if t is not None:
+                _check16(t, nm, shape, dt, dev)
+        _raise(_lib.mx_linear_act(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(z), _ptr(y), m, n, k, _DTYPES[dt],
+                                  act, _status_on(dev_status, dev), s), "mx_linear_act")
+    return y if z is None else (y, z)
+
+
+def mx_linear_act_backward_workspace_bytes(m: int, n: int) -> int:
+    """Bytes of the workspace that dbias needs."""
+    return int(_lib.mx_linear_act_backward_workspace_bytes(m, n))
+
+
+def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None,
+                           z: torch.Tensor | None = None, activation: str = "none", bias_grad: bool = False,
+                           dz: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                           dw: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                           stream=None):
+    """Gradients of mx_linear_act from dy [M, N] and the z it returned (not
+    needed with activation "none").  Returns (dx [M, K], dw [N, K], dbias [N]);
+    dx is None without ``w`` and dw without ``x`` (a frozen layer, or one whose
+    input needs no gradient), dbias is None unless ``bias_grad`` or an output
+    ``dbias``.  The residual's gradient is dy.  ``dz`` [M, N] receives
+    dy * act'(z)."""
+    dt = _operand16(dy, "dy", 2)
+    act = _activation(activation)
+    m, n = dy.shape
+    dev = dy.device
+    if x is None and w is None:
+        raise ValueError("x (for dw) or w (for dx) must be given")
+    if (x is None and dw is not None) or (w is None and dx is not None):
+        raise ValueError("dw needs x, dx needs w")
+    for t, nm in ((x, "x"), (w, "w")):
+        if t is not None:
+            _operand16(t, nm, 2)
+    k = x.shape[1] if x is not None else w.shape[1]
+    if act != 0 and z is None:
+        raise ValueError(f"activation {activation!r} needs z")
+    for t, nm, shape in ((x, "x", (m, k)), (w, "w", (n, k)), (z, "z", (m, n))):
+        if t is not None:
+            _check16(t, nm, shape, dt, dev)
+    need = mx_linear_act_backward_workspace_bytes(m, n)
+    with _launch_on(dy, stream) as s:
+        if w is not None and dx is None:
+            dx = torch.empty((m, k), dtype=dt, device=dev)
+        if x is not None and dw is None:
+            dw = torch.empty((n, k), dtype=dt, device=dev)
+        if bias_grad and dbias is None:
+            dbias = torch.empty(n, dtype=dt, device=dev)
+        if act != 0 and dz is None:
+            dz = torch.empty((m, n), dtype=dt, device=dev)
+        if dbias is not None and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        for t, nm, shape in ((dx, "dx", (m, k)), (dw, "dw", (n, k)), (dbias, "dbias", (n,)), (dz, "dz", (m, n))):
+            if t is not None:
+                _check16(t, nm, shape, dt, dev)
+        if workspace is not None:
+            _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _raise(_lib.mx_linear_act_backward(_ptr(dy), _ptr(z), _ptr(x), _ptr(w), _ptr(dz), _ptr(dx), _ptr(dw),
+                                           _ptr(dbias), m, n, k, _DTYPES[dt], act, _ptr(workspace),
+                                           0 if workspace is None else workspace.numel(),
+                                           _status_on(dev_status, dev), s), "mx_linear_act_backward")
+    return dx, dw, dbias
+
+
+def _offsets(group_offsets, groups, device):
+    _check16(group_offsets, "group_offsets", (groups + 1,), torch.int32, device)
+
+
+def mx_grouped_gemm_ragged(a: torch.Tensor, b: torch.Tensor, group_offsets: torch.Tensor,
+                           d: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """16-bit products grouped by expert: a [M_total, K], b [E, N, K],
+    group_offsets int32 [E+1] (any non-decreasing row numbers, on the device) ->
+    d [M_total, N] with d[i] = a[i] b[e]^T for the rows of expert e.  Rows
+    outside [offsets[0], offsets[E]) are left as they were."""
+    dt = _operand16(a, "a", 2)
+    _operand16(b, "b", 3)
+    m, k = a.shape
+    groups, n = b.shape[0], b.shape[1]
+    dev = a.device
+    _check16(b, "b", (groups, n, k), dt, dev)
+    _offsets(group_offsets, groups, dev)
+    with _launch_on(a, stream) as s:
+        d = torch.empty((m, n), dtype=dt, device=dev) if d is None else d
+        _check16(d, "d", (m, n), dt, dev)
+        _raise(_lib.mx_grouped_gemm_ragged(_ptr(a), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt], _ptr(d),
+                                           _status_on(dev_status, dev), s), "mx_grouped_gemm_ragged")
+    return d
+
+
+def mx_grouped_gemm_ragged_dgrad(dd: torch.Tensor, b: torch.Tensor, group_offsets: torch.Tensor,
+                                 da: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                                 stream=None) -> torch.Tensor:
+    """Input gradient of mx_grouped_gemm_ragged: dd [M_total, N], b [E, N, K] ->
+    da [M_total, K] with da[i] = dd[i] b[e].  Rows outside the groups are left
+    as they were."""
+    dt = _operand16(dd, "dd", 2)
+    _operand16(b, "b", 3)
+    m, n = dd.shape
+    groups, k = b.shape[0], b.shape[2]
+    dev = dd.device
+    _check16(b, "b", (groups, n, k), dt, dev)
+    _offsets(group_offsets, groups, dev)
+    with _launch_on(dd, stream) as s:
+        da = torch.empty((m, k), dtype=dt, device=dev) if da is None else da
+        _check16(da, "da", (m, k), dt, dev)
+        _raise(_lib.mx_grouped_gemm_ragged_dgrad(_ptr(dd), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
+                                                 _ptr(da), _status_on(dev_status, dev), s),
+               "mx_grouped_gemm_ragged_dgrad")
+    return da
+
+
+def mx_grouped_gemm_ragged_wgrad(dd: torch.Tensor, a: torch.Tensor, group_offsets: torch.Tensor,
+                                 db: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                                 dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Weight gradient of mx_grouped_gemm_ragged: dd [M_total, N], a [M_total, K]
+    -> db [E, N, K], the sum over expert e's rows of dd[i]^T a[i] (zeros for an
+    expert without rows), in the operands' type or FP32 (``out_dtype``)."""
+    dt = _operand16(dd, "dd", 2)
+    _operand16(a, "a", 2)
+    m, n = dd.shape
+    k = a.shape[1]
+    dev = dd.device
+    _check16(a, "a", (m, k), dt, dev)
+    if not isinstance(group_offsets, torch.Tensor) or group_offsets.dim() != 1 or group_offsets.numel() < 1:
+        raise ValueError("group_offsets must be a 1-D tensor of groups + 1 entries")
+    groups = group_offsets.numel() - 1
+    _offsets(group_offsets, groups, dev)
+    out_dtype = (dt if db is None else db.dtype) if out_dtype is None else out_dtype
+    if out_dtype not in (dt, torch.float32):
+        raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
+    with _launch_on(dd, stream) as s:
+        db = torch.empty((groups, n, k), dtype=out_dtype, device=dev) if db is None else db
+        _check16(db, "db", (groups, n, k), out_dtype, dev)
+        _raise(_lib.mx_grouped_gemm_ragged_wgrad(_ptr(dd), _ptr(a), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
+                                                 _DTYPES[out_dtype], _ptr(db), _status_on(dev_status, dev), s),
+               "mx_grouped_gemm_ragged_wgrad")
+    return db
+
+
+def mx_orthogonalize_workspace_bytes(batch: int, m: int, n: int, dtype: torch.dtype = torch.bfloat16,
+                                     steps: int = 5) -> int:
+    """Bytes of the workspace mx_orthogonalize needs for [batch, m, n] of ``dtype``."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    return int(_lib.mx_orthogonalize_workspace_bytes(batch, m, n, _DTYPES[dtype], steps))
+
+
+def mx_orthogonalize(g: torch.Tensor, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of g ([m, n] or [batch, m, n], BF16 or
+    FP32): X = g / (|g|_F + eps), then ``steps`` times X = a X + (b A + c A^2) X
+    with A = X X^T and (a, b, c) = ``coeffs`` (one triple, or one per step).
+    Returns BF16 of g's shape.  ``workspace``: uint8, at least
+    mx_orthogonalize_workspace_bytes(...); calls that may run at the same time
+    (two streams, two captured graphs) need one each."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    if g.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"g must be torch.bfloat16 or torch.float32, got {g.dtype}")
+    _check(g, g.dtype, "g")
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be 2-D [m, n] or 3-D [batch, m, n]")
+    flat = [float(v) for c in coeffs for v in (c if isinstance(c, (tuple, list)) else (c,))]
+    if not isinstance(steps, int) or steps < 1:
+        raise ValueError("steps must be a positive integer")
+    if len(flat) == 3:
+        flat *= steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coeffs must be one (a, b, c) or {steps} of them")
+    batch = 1 if g.dim() == 2 else g.shape[0]
+    m, n = g.shape[-2], g.shape[-1]
+    dev = g.device
+    need = mx_orthogonalize_workspace_bytes(batch, m, n, g.dtype, steps)
+    with _launch_on(g, stream) as s:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        _check16(out, "out", g.shape, torch.bfloat16, dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _raise(_lib.mx_orthogonalize(_ptr(g), _DTYPES[g.dtype], _ptr(out), batch, m, n, steps,
+                                     (ctypes.c_float * len(flat))(*flat), eps, _ptr(workspace), workspace.numel(),
+                                     _status_on(dev_status, dev), s), "mx_orthogonalize")
     return out
 
 

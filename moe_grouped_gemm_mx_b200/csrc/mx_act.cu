@@ -1,0 +1,128 @@
+// mx_act.cu -- the element-wise part of mx_linear_act's backward pass:
+//
+//   dZ = dY * act'(Z)   (one rounding to the operand type)
+//   dbias[j] = sum_i dY[i, j] * act'(Z[i, j])   (FP32 products and sums)
+//
+// One pass over dY and Z: each thread keeps eight columns (16-byte loads and
+// stores) over a chunk of rows and leaves their sums; a second small launch
+// adds the chunks' sums in order, so the result does not change from call to
+// call.  Bound by its bytes.
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "mx_gemm16.cuh"
+#include "mx_launch.h"
+
+namespace mxk {
+
+constexpr int kActCols = 256;  // columns of a block: 32 threads of 8
+constexpr int kActRows = 8;    // rows a block works on at one time
+
+template <int ACT>
+__global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __restrict__ dy,
+                                                           const uint16_t* __restrict__ z, uint16_t* __restrict__ dz,
+                                                           float* __restrict__ partial, int64_t m, int n, int64_t chunk,
+                                                           int fp16) {
+  __shared__ float sums[kActRows][kActCols + 1];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int col = blockIdx.x * kActCols + tx * 8;
+  const int64_t r0 = blockIdx.y * chunk;
+  const int64_t r1 = r0 + chunk < m ? r0 + chunk : m;
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  if (col < n) {
+#pragma unroll 4
+    for (int64_t r = r0 + ty; r < r1; r += kActRows) {
+      const int64_t at = r * n + col;
+      float g[8];
+      load8(dy + at, fp16, g);
+      if constexpr (ACT != 0) {
+        float x[8];
+        load8(z + at, fp16, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] *= act_grad_f32(x[j], ACT);
+        *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack16(g[0], g[1], fp16), pack16(g[2], g[3], fp16),
+                                                        pack16(g[4], g[5], fp16), pack16(g[6], g[7], fp16));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += g[j];
+    }
+  }
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[ty][tx * 8 + j] = s[j];
+  __syncthreads();
+  const int c = blockIdx.x * kActCols + threadIdx.x;
+  if (c < n) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kActRows; ++i) t += sums[i][threadIdx.x];
+    partial[static_cast<int64_t>(blockIdx.y) * n + c] = t;
+  }
+}
+
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float* __restrict__ partial, uint16_t* __restrict__ dbias,
+                                                       int n, int chunks, int fp16) {
+  __shared__ float sums[8][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + tx;
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  float s = 0.0f;
+  if (col < n)
+    for (int i = ty; i < chunks; i += 8) s += partial[static_cast<int64_t>(i) * n + col];
+  sums[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && col < n) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sums[i][tx];
+    dbias[col] = static_cast<uint16_t>(pack16(s, 0.0f, fp16) & 0xFFFFu);
+  }
+}
+
+static cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute (&attr)[1]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Chunks of rows: enough blocks for the GPU, at most 64 sums a column to add.
+int64_t act_backward_chunks(int64_t m) {
+  const int64_t c = (m + 31) / 32;
+  return c < 64 ? c : 64;
+}
+
+cudaError_t launch_act_backward(const void* dy, const void* z, void* dz, void* dbias, float* partial, int64_t m,
+                                int64_t n, int act, int fp16, cudaStream_t stream) {
+  const int64_t chunks = act_backward_chunks(m);
+  const int64_t chunk = (m + chunks - 1) / chunks;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((n + kActCols - 1) / kActCols),
+                                           static_cast<unsigned>((m + chunk - 1) / chunk), 1),
+                                      256, stream, attr);
+  const uint16_t* y16 = static_cast<const uint16_t*>(dy);
+  const uint16_t* z16 = static_cast<const uint16_t*>(z);
+  uint16_t* d16 = static_cast<uint16_t*>(dz);
+  float* part = dbias ? partial : nullptr;
+  cudaError_t e;
+  switch (act) {
+    case 0: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<0>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+    case 1: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<1>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+    case 2: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<2>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+    case 3: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<3>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+    default: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<4>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+  }
+  if (e != cudaSuccess || !dbias) return e;
+  cfg = pdl_config(dim3(static_cast<unsigned>((n + 31) / 32), 1, 1), 256, stream, attr);
+  return cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(part), static_cast<uint16_t*>(dbias),
+                            static_cast<int>(n), static_cast<int>((m + chunk - 1) / chunk), fp16);
+}
+
+}  // namespace mxk

@@ -4,7 +4,9 @@
 // 4-byte internal status word below.
 #include <cuda_runtime.h>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/mx.h"
 
@@ -610,6 +612,257 @@ mx_status mx_moe_combine_peer(const void* const* y_peers, int32_t ranks, int64_t
   int32_t* status = dev_status ? dev_status : internal_status_ptr();
   return from_cuda(mxk::launch_moe_combine(nullptr, y_peers, src_rank, ranks, y_rows, n_cols, src_row, w, tokens,
                                            topk, out_bf16, status, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ 16-bit products
+
+// Row and tile numbers of the 16-bit kernels are 32-bit, with room for a tile
+// behind the last row.
+constexpr int64_t kMaxDim16 = (int64_t(1) << 31) - 1024;
+
+static bool dtype16(int32_t t) { return t == MX_BF16 || t == MX_FP16; }
+
+static bool misaligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return true;
+  return false;
+}
+
+// Device and status word of a call that launches.
+static mx_status launch_context(int32_t* dev_status, int* sms, int32_t** status) {
+  *sms = num_sms();
+  if (*sms <= 0) return MX_ERR_CUDA;
+  *status = dev_status ? dev_status : internal_status_ptr();
+  return *status ? MX_OK : MX_ERR_CUDA;
+}
+
+static mx_status zero_bytes(void* p, int64_t bytes, mx_stream_t stream) {
+  return from_cuda(cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), static_cast<cudaStream_t>(stream)));
+}
+
+// A dense product of row-major tensors: D [m, n] = A B^T with A [m, k] (a_mn: [k, m]), B [n, k] (b_mn: [k, n]).
+static mxk::Gemm16 dense16(const void* a, int a_mn, const void* b, int b_mn, void* d, int64_t m, int64_t n, int64_t k,
+                           int32_t dtype, int32_t* status) {
+  mxk::Gemm16 g = {};
+  g.a = a;
+  g.a_mn = a_mn;
+  g.a_ld = a_mn ? m : k;
+  g.a_batch = m * k;
+  g.b = b;
+  g.b_mn = b_mn;
+  g.b_ld = b_mn ? n : k;
+  g.b_batch = n * k;
+  g.d = d;
+  g.d_ld = n;
+  g.d_batch = m * n;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.groups = 1;
+  g.op_fp16 = dtype == MX_FP16;
+  g.out_type = dtype;
+  g.status = status;
+  return g;
+}
+
+static mx_status check_linear(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act) {
+  if (m < 0 || n < 0 || k < 0 || !dtype16(dtype) || act < MX_ACT_NONE || act > MX_ACT_GELU_TANH)
+    return MX_ERR_INVALID_ARGUMENT;
+  if (k == 0 || k % 8 != 0 || n % 8 != 0 || m > kMaxDim16 || n > kMaxDim16 || k > kMaxDim16)
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  return MX_OK;
+}
+
+mx_status mx_linear_act(const void* x, const void* w, const void* bias, const void* residual, void* z, void* y,
+                        int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act, int32_t* dev_status,
+                        mx_stream_t stream) {
+  mx_status st = check_linear(m, n, k, dtype, act);
+  if (st != MX_OK || m == 0 || n == 0) return st;
+  if (!x || !w || !y) return MX_ERR_INVALID_ARGUMENT;
+  if (misaligned16({x, w, bias, residual, z, y})) return MX_ERR_MISALIGNED;
+  int sms;
+  int32_t* status;
+  st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  mxk::Gemm16 g = dense16(x, 0, w, 0, y, m, n, k, dtype, status);
+  g.epi = 1;
+  g.bias = bias;
+  g.res = residual;
+  g.res_ld = n;
+  g.z = z;
+  g.act = act;
+  return from_cuda(mxk::launch_gemm16(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mx_linear_act_backward_workspace_bytes(int64_t m, int64_t n) {
+  if (m <= 0 || n <= 0) return 0;
+  return static_cast<size_t>(mxk::act_backward_chunks(m) * n) * sizeof(float);
+}
+
+mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, const void* w, void* dz, void* dx,
+                                 void* dw, void* dbias, int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, mx_stream_t stream) {
+  mx_status st = check_linear(m, n, k, dtype, act);
+  if (st != MX_OK) return st;
+  if (misaligned16({dy, z, x, w, dz, dx, dw, dbias, workspace})) return MX_ERR_MISALIGNED;
+  if (m == 0 || n == 0) {  // empty sums
+    if (m > 0 && dx) return zero_bytes(dx, m * k * 2, stream);
+    if (n > 0 && dw) st = zero_bytes(dw, n * k * 2, stream);
+    if (st == MX_OK && n > 0 && dbias) st = zero_bytes(dbias, n * 2, stream);
+    return st;
+  }
+  if (!dy || (dx && !w) || (dw && !x) || (act != MX_ACT_NONE && (!z || !dz))) return MX_ERR_INVALID_ARGUMENT;
+  if (dbias && (!workspace || workspace_bytes < mx_linear_act_backward_workspace_bytes(m, n)))
+    return MX_ERR_INVALID_ARGUMENT;
+  if (!dx && !dw && !dbias) return MX_OK;
+  int sms;
+  int32_t* status;
+  st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (act != MX_ACT_NONE || dbias)
+    e = mxk::launch_act_backward(dy, z, dz, dbias, static_cast<float*>(workspace), m, n, act, dtype == MX_FP16, s);
+  const void* g = act != MX_ACT_NONE ? dz : dy;
+  if (e == cudaSuccess && dx) e = mxk::launch_gemm16(dense16(g, 0, w, 1, dx, m, k, n, dtype, status), sms, s);
+  if (e == cudaSuccess && dw) e = mxk::launch_gemm16(dense16(g, 1, x, 1, dw, n, k, m, dtype, status), sms, s);
+  return from_cuda(e);
+}
+
+static mx_status check_ragged(const void* a, const void* b, const int32_t* group_offsets, int32_t groups,
+                              int64_t m_total, int64_t n, int64_t k, int32_t dtype, const void* d, bool* empty) {
+  *empty = false;
+  if (groups < 0 || m_total < 0 || n < 0 || k < 0 || !dtype16(dtype)) return MX_ERR_INVALID_ARGUMENT;
+  if (n == 0 || k == 0 || n % 8 != 0 || k % 8 != 0 || n > kMaxDim16 || k > kMaxDim16 || m_total > kMaxDim16 ||
+      groups > kMaxGroups)
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  if (groups == 0 || m_total == 0) {
+    *empty = true;
+    return MX_OK;
+  }
+  if (!a || !b || !d || !group_offsets) return MX_ERR_INVALID_ARGUMENT;
+  if (misaligned16({a, b, d}) || (reinterpret_cast<uintptr_t>(group_offsets) & 3u)) return MX_ERR_MISALIGNED;
+  return MX_OK;
+}
+
+mx_status mx_grouped_gemm_ragged(const void* a, const void* b, const int32_t* group_offsets, int32_t groups,
+                                 int64_t m_total, int64_t n, int64_t k, int32_t dtype, void* d, int32_t* dev_status,
+                                 mx_stream_t stream) {
+  bool empty;
+  mx_status st = check_ragged(a, b, group_offsets, groups, m_total, n, k, dtype, d, &empty);
+  if (st != MX_OK || empty) return st;
+  int sms;
+  int32_t* status;
+  st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  mxk::Gemm16 g = dense16(a, 0, b, 0, d, m_total, n, k, dtype, status);
+  g.mode = 1;
+  g.groups = groups;
+  g.group_offsets = group_offsets;
+  return from_cuda(mxk::launch_gemm16(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_grouped_gemm_ragged_dgrad(const void* dd, const void* b, const int32_t* group_offsets, int32_t groups,
+                                       int64_t m_total, int64_t n, int64_t k, int32_t dtype, void* da,
+                                       int32_t* dev_status, mx_stream_t stream) {
+  bool empty;
+  mx_status st = check_ragged(dd, b, group_offsets, groups, m_total, n, k, dtype, da, &empty);
+  if (st != MX_OK || empty) return st;
+  int sms;
+  int32_t* status;
+  st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  mxk::Gemm16 g = dense16(dd, 0, b, 1, da, m_total, k, n, dtype, status);
+  g.mode = 1;
+  g.groups = groups;
+  g.group_offsets = group_offsets;
+  return from_cuda(mxk::launch_gemm16(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+mx_status mx_grouped_gemm_ragged_wgrad(const void* dd, const void* a, const int32_t* group_offsets, int32_t groups,
+                                       int64_t m_total, int64_t n, int64_t k, int32_t dtype, int32_t out_dtype,
+                                       void* db, int32_t* dev_status, mx_stream_t stream) {
+  if (out_dtype != dtype && out_dtype != MX_FP32) return MX_ERR_INVALID_ARGUMENT;
+  bool empty;
+  mx_status st = check_ragged(dd, a, group_offsets, groups, m_total, n, k, dtype, db, &empty);
+  if (st != MX_OK) return st;
+  if (empty) {
+    if (groups == 0) return MX_OK;
+    if (!db) return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned16(db)) return MX_ERR_MISALIGNED;
+    return zero_bytes(db, groups * n * k * (out_dtype == MX_FP32 ? 4 : 2), stream);
+  }
+  int sms;
+  int32_t* status;
+  st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  mxk::Gemm16 g = dense16(dd, 1, a, 1, db, n, k, m_total, dtype, status);
+  g.mode = 2;
+  g.groups = groups;
+  g.group_offsets = group_offsets;
+  g.out_type = out_dtype;
+  return from_cuda(mxk::launch_gemm16(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Do the steps keep every matrix inside FP16's range?  The singular values lie
+// in [0, u]; their next bound is the largest |a s + b s^3 + c s^5| there, and the
+// entries of A, B and a I + B are at most the largest |s^2|, |b s^2 + c s^4| and
+// |a + b s^2 + c s^4| (of symmetric matrices no entry exceeds the norm).
+static bool ns_coefficients_fit(const float* coeffs, int steps) {
+  double u = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    const double a = coeffs[3 * i], b = coeffs[3 * i + 1], c = coeffs[3 * i + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    double largest = 0.0, poly = 0.0;
+    auto look = [&](double t) {  // t = s^2
+      if (!(t >= 0.0 && t <= u * u)) return;
+      const double q = b * t + c * t * t;
+      largest = std::fmax(largest, std::fabs((a + q) * std::sqrt(t)));
+      poly = std::fmax(poly, std::fmax(std::fabs(q), std::fabs(a + q)));
+    };
+    look(0.0);
+    look(u * u);
+    if (c != 0.0) {
+      look(-b / (2.0 * c));                       // extremum of b t + c t^2
+      const double disc = 9.0 * b * b - 20.0 * a * c;  // of the odd quintic: 5 c t^2 + 3 b t + a = 0
+      if (disc >= 0.0) {
+        look((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+        look((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+      }
+    } else if (b != 0.0) {
+      look(-a / (3.0 * b));
+    }
+    if (poly > 15.5) return false;
+    u = 1.01 * largest;  // room for the roundings
+    if (!(u <= 3.9)) return false;
+    if (u == 0.0) u = 1e-3;
+  }
+  return true;
+}
+
+size_t mx_orthogonalize_workspace_bytes(int64_t batch, int64_t m, int64_t n, int32_t g_dtype, int32_t steps) {
+  if (batch <= 0 || m <= 0 || n <= 0 || steps <= 0 || batch > 65535 || m > (int64_t(1) << 20) || n > (int64_t(1) << 20))
+    return 0;
+  return mxk::ns_workspace_bytes(batch, m, n, g_dtype == MX_FP32, steps);
+}
+
+mx_status mx_orthogonalize(const void* g, int32_t g_dtype, void* out_bf16, int64_t batch, int64_t m, int64_t n,
+                           int32_t steps, const float* coeffs, float eps, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, mx_stream_t stream) {
+  if (batch < 0 || m < 0 || n < 0 || (g_dtype != MX_BF16 && g_dtype != MX_FP32) || steps < 1 || steps > 16 || !coeffs ||
+      !(eps >= 0.0f) || !std::isfinite(eps) || !ns_coefficients_fit(coeffs, steps))
+    return MX_ERR_INVALID_ARGUMENT;
+  if (batch > 65535 || m > (int64_t(1) << 20) || n > (int64_t(1) << 20)) return MX_ERR_UNSUPPORTED_SHAPE;
+  if (batch == 0 || m == 0 || n == 0) return MX_OK;
+  if (!g || !out_bf16 || !workspace) return MX_ERR_INVALID_ARGUMENT;
+  if (misaligned16({g, out_bf16}) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MX_ERR_MISALIGNED;
+  if (workspace_bytes < mxk::ns_workspace_bytes(batch, m, n, g_dtype == MX_FP32, steps)) return MX_ERR_INVALID_ARGUMENT;
+  int sms;
+  int32_t* status;
+  mx_status st = launch_context(dev_status, &sms, &status);
+  if (st != MX_OK) return st;
+  mxk::OrthoProblem q{g, out_bf16, workspace, status, coeffs, batch, m, n, steps, eps, g_dtype == MX_FP32};
+  return from_cuda(mxk::launch_orthogonalize(q, sms, static_cast<cudaStream_t>(stream)));
 }
 
 mx_status mx_set_wait_limit_ns(uint64_t ns) {

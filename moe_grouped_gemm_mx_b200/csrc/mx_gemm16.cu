@@ -1,0 +1,813 @@
+// mx_gemm16.cu -- GEMM on BF16 / FP16 operands for sm_100a, dense (batched),
+// grouped along M with ragged groups, and grouped along K with ragged groups.
+//
+// Two kernels compute the same thing (mx_gemm16.cuh):
+//
+//  g16_pair_kernel  two CTAs of a cluster share a 256 x 256 tile of D
+//    (tcgen05.mma cta_group::2, 128 rows of A and of B in each CTA's shared
+//    memory), persistent, the accumulator double-buffered in TMEM so that the
+//    epilogue of one tile runs beside the MMAs of the next.
+//      warp 0      TMA producer (both CTAs): 128 elements of K per stage
+//      warp 1      MMA issuer (leader), K = 16 per instruction
+//      warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
+//      warp 10     ragged K only (both CTAs): clears the rows of the stage that
+//                  lie behind the group's last token before the MMAs read them
+//
+//  g16_small_kernel  one CTA per 128 x 128 tile, K split over a cluster of 1, 2,
+//    4 or 8 CTAs whose partial sums meet in distributed shared memory (in a
+//    fixed order), two CTAs to an SM.  For products that would leave most SMs
+//    idle in 256 x 256 tiles, where the operands' bytes bound the time.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <atomic>
+#include <cstdint>
+#include <cstdlib>
+
+#include "mx_gemm16.cuh"
+#include "mx_launch.h"
+
+namespace mxk {
+
+// ======================================================================= CTA-pair kernel
+
+constexpr int kP16Stages = 3;
+constexpr int kP16EpiWarps = 8;
+constexpr int kP16Threads = 32 * (2 + kP16EpiWarps + 1);
+constexpr int kP16TM = 256, kP16TN = 256;
+constexpr int kP16K = 128;  // elements of K per stage
+
+struct P16Layout {
+  static constexpr int CHUNK = 128 * 128;           // 16 KB: 128 rows of 128 bytes
+  static constexpr int OP_BYTES = 2 * CHUNK;        // one operand's half tile of a stage
+  static constexpr int OFF_A = 0;
+  static constexpr int OFF_B = OFF_A + kP16Stages * OP_BYTES;
+  static constexpr int OFF_STG = OFF_B + kP16Stages * OP_BYTES;
+  static constexpr int STG_BYTES = 32 * 64;         // per epilogue warp: 32 rows of 64 bytes
+  static constexpr int OFF_BAR = OFF_STG + kP16EpiWarps * STG_BYTES;
+  // full, empty, ready per stage; accumulator full and empty (2 each); drain
+  static constexpr int NUM_BARS = 3 * kP16Stages + 5;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_TAB = OFF_MISC + 16;
+  static constexpr int BYTES = OFF_TAB + (kMaxGroups + 1) * 4;
+  static constexpr int ALLOC = BYTES + 1024;
+  static_assert(OFF_STG % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(ALLOC <= 232448, "shared memory budget");
+};
+
+template <int EPI>
+__global__ void __launch_bounds__(kP16Threads, 1)
+    g16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_z,
+                    const G16Args args) {
+  using L = P16Layout;
+  constexpr int S = kP16Stages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x) >> 1;
+  const int npairs = static_cast<int>(gridDim.x) >> 1;
+  const bool ragged_k = args.mode == kRaggedK;
+
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile uint32_t* tmem_slot = misc + 0;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + L::OFF_TAB);
+
+  auto full_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * s; };
+  auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
+  auto ready_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (2 * S + s); };
+  auto accf_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (3 * S + b); };
+  auto acce_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (3 * S + 2 + b); };
+  const uint32_t drain_bar = sbase + L::OFF_BAR + 8u * (3 * S + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);   // one arrival that announces the bytes
+      mbar_init(empty_bar(s), 1);  // the leader's commit, multicast to both CTAs
+      mbar_init(ready_bar(s), 2);  // ragged K: one arrival from each CTA's warp 10, on the leader
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1);
+      mbar_init(acce_bar(b), 2 * kP16EpiWarps);  // one lane of each epilogue warp of both CTAs, on the leader
+    }
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmap_a);
+    prefetch_tmap(&tmap_b);
+    prefetch_tmap(&tmap_d);
+  }
+  pdl_launch_dependents();
+  pdl_wait_prior();
+
+  int bad = 0;
+  if (args.mode != kBatched) {
+    bad = g16_offsets_bad(args, args.mode == kRaggedM ? args.m : args.k);
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0 && rank == 0) report(args.status, 0x1);
+    if (args.mode == kRaggedM && warp == 0) g16_prefix<kP16TM>(args, tab, bad);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+    tmem_relinquish_pair();
+  }
+  // barriers initialised and TMEM allocated in BOTH CTAs before any cross-CTA traffic
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = bad ? 0 : args.mode == kRaggedM ? tab[args.groups] : args.groups * g16_tiles_per_entry(args);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ===== TMA producer.  Both CTAs' loads complete on the leader's full
+      // barrier; with ragged K on the CTA's own, which its warp 10 waits for.
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        const G16Tile tl = g16_decode<kP16TM>(args, tab, t);
+        const int a_mn0 = tl.row0 + 128 * static_cast<int>(rank);
+        const int b_mn0 = tl.nb * kP16TN + 128 * static_cast<int>(rank);
+        const int a_z = args.mode == kBatched ? tl.group : 0;
+        const int b_z = args.b_per_group ? tl.group : 0;
+        int k0, kn;
+        g16_k_range(args, tl.group, k0, kn);
+        for (int kk = 0; kk < kn; kk += kP16K) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+          // a K-major operand's second chunk of 64 is not needed when K ends before it
+          const int k_chunks = kn - kk > 64 ? 2 : 1;
+          const uint32_t bytes = (args.a_mn ? L::OP_BYTES : k_chunks * L::CHUNK) +
+                                 (args.b_mn ? L::OP_BYTES : k_chunks * L::CHUNK);
+          const uint32_t fb = ragged_k ? full_bar(stage) : map_to_rank(full_bar(stage), 0);
+          if (ragged_k)
+            mbar_arrive_expect_tx(full_bar(stage), bytes);
+          else if (rank == 0)
+            mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+          const uint32_t sa = sbase + L::OFF_A + stage * L::OP_BYTES;
+          const uint32_t sb = sbase + L::OFF_B + stage * L::OP_BYTES;
+          if (ragged_k) {  // both operands MN-major, completing on this CTA's barrier
+            tma_load_3d(sa, &tmap_a, fb, a_mn0, k0 + kk, a_z);
+            tma_load_3d(sa + L::CHUNK, &tmap_a, fb, a_mn0 + 64, k0 + kk, a_z);
+            tma_load_3d(sb, &tmap_b, fb, b_mn0, k0 + kk, b_z);
+            tma_load_3d(sb + L::CHUNK, &tmap_b, fb, b_mn0 + 64, k0 + kk, b_z);
+          } else {
+            if (args.a_mn) {
+              tma_load_3d_pair(sa, &tmap_a, fb, a_mn0, kk, a_z);
+              tma_load_3d_pair(sa + L::CHUNK, &tmap_a, fb, a_mn0 + 64, kk, a_z);
+            } else {
+              tma_load_3d_pair(sa, &tmap_a, fb, kk, a_mn0, a_z);
+              if (k_chunks == 2) tma_load_3d_pair(sa + L::CHUNK, &tmap_a, fb, kk + 64, a_mn0, a_z);
+            }
+            if (args.b_mn) {
+              tma_load_3d_pair(sb, &tmap_b, fb, b_mn0, kk, b_z);
+              tma_load_3d_pair(sb + L::CHUNK, &tmap_b, fb, b_mn0 + 64, kk, b_z);
+            } else {
+              tma_load_3d_pair(sb, &tmap_b, fb, kk, b_mn0, b_z);
+              if (k_chunks == 2) tma_load_3d_pair(sb + L::CHUNK, &tmap_b, fb, kk + 64, b_mn0, b_z);
+            }
+          }
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {  // loads already in flight land during the teardown's linger
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ===== MMA issuer: up to 8 pair MMAs of K = 16 per stage
+      const uint32_t idesc = idesc_f16(kP16TM, kP16TN, args.op_fp16, args.a_mn, args.b_mn);
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs, ++it) {
+        const int buf = it & 1;
+        if (!mbar_wait_cluster(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t acc = tmem_base + buf * kP16TN;
+        int k0, kn;
+        g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
+        for (int kk = 0; kk < kn; kk += kP16K) {
+          const bool got = ragged_k ? mbar_wait_cluster(ready_bar(stage), phase, abort_flag, args.wait_ns)
+                                    : mbar_wait(full_bar(stage), phase, abort_flag, args.wait_ns);
+          if (!got) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = sbase + L::OFF_A + stage * L::OP_BYTES;
+          const uint32_t sb = sbase + L::OFF_B + stage * L::OP_BYTES;
+          const int left = kn - kk;
+#pragma unroll
+          for (int s = 0; s < kP16K / 16; ++s) {
+            if (s * 16 < left) {  // what is behind K's end is zeros or was not loaded
+              const uint32_t k_off = (s >> 2) * L::CHUNK + (s & 3) * 32;
+              const uint64_t da = args.a_mn ? desc_mnmajor_sw128(sa + s * 2048, L::CHUNK) : desc_kmajor_sw128(sa + k_off);
+              const uint64_t db = args.b_mn ? desc_mnmajor_sw128(sb + s * 2048, L::CHUNK) : desc_kmajor_sw128(sb + k_off);
+              tc_mma_pair_f16(acc, da, db, idesc, (kk | s) != 0 ? 1u : 0u);
+            }
+          }
+          tc_commit_pair_multicast(empty_bar(stage), 0x3);
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair_multicast(accf_bar(buf), 0x3);
+      }
+      if (!ok) {
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+      // every pair MMA issued must finish before either CTA frees its TMEM
+      tc_commit_pair_multicast(drain_bar, 0x1);
+      mbar_wait(drain_bar, 0, nullptr, 100000000ull);
+    }
+  } else if (warp == 2 + kP16EpiWarps) {
+    if (ragged_k) {
+      // ===== the K rows behind a group's last token belong to the next group:
+      // cleared up to the end of the MMAs' last step of 16 in both operands, so
+      // that whatever they hold (infinities included) adds nothing
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        int k0, kn;
+        g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
+        for (int kk = 0; kk < kn; kk += kP16K) {
+          ok = mbar_wait(full_bar(stage), phase, abort_flag, args.wait_ns);
+          if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+          const int left = kn - kk;
+          if (left < kP16K && (left & 15) != 0) {
+            const int rows = 16 - (left & 15);
+            // 4 tiles (A's and B's two 64-column chunks) x rows x 8 pieces of 16 bytes
+            for (int i = lane; i < 4 * rows * 8; i += 32) {
+              const int piece = i & 7, row = (i >> 3) % rows, tile = (i >> 3) / rows;
+              const uint32_t at = sbase + (tile < 2 ? L::OFF_A : L::OFF_B) + stage * L::OP_BYTES +
+                                  (tile & 1) * L::CHUNK + (left + row) * 128 + piece * 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(ready_bar(stage), 0));
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok && lane == 0) {
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+    }
+  } else {
+    // ===== epilogue: rows of the warp's TMEM lane quarter, one half of the columns
+    const int ew = warp - 2;
+    const int quarter = warp & 3;
+    const int half = ew >> 2;
+    const uint32_t stg = sbase + L::OFF_STG + ew * L::STG_BYTES;
+    const int h = args.out_type == 1;
+    int it = 0;
+    for (int t = pair; t < total; t += npairs, ++it) {
+      const int buf = it & 1;
+      const bool got = mbar_wait(accf_bar(buf), (it >> 1) & 1u, abort_flag, args.wait_ns);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        if (lane == 0) {
+          report(args.status, 0x4);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      tc_fence_after();
+      const G16Tile tl = g16_decode<kP16TM>(args, tab, t);
+      int k0, kn;
+      g16_k_range(args, tl.group, k0, kn);
+      const int row_w = tl.row0 + 128 * static_cast<int>(rank) + 32 * quarter;  // the warp's first row
+      const int row = row_w + lane;
+      const bool valid = row < tl.rows_end;
+      // TMA clips rows behind the tensor's last but not behind a group's
+      const bool tma = args.tma_store && (args.mode != kRaggedM || row_w + 32 <= tl.rows_end);
+      const uint32_t t_row = tmem_base + buf * kP16TN + (static_cast<uint32_t>(quarter * 32) << 16);
+      const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+      if (row_w < tl.rows_end) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col_t = half * 128 + c * 32;
+          const int col0 = tl.nb * kP16TN + col_t;
+          if (col0 >= args.n) break;
+          uint32_t raw[32];
+          tc_ld_32x32b_x32(t_row + col_t, raw);
+          tc_wait_ld();
+          float v[32], second[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = kn == 0 ? 0.0f : __uint_as_float(raw[j]);  // no MMA wrote an empty sum
+          g16_epilogue<EPI, 32>(args, v, second, tl.group, row, col0, valid, scale);
+          if (!tma) {
+            if (valid) {
+              g16_store_row<32>(args, args.d, v, tl.group, row, col0);
+              if (EPI != kEpiPlain && args.z != nullptr) g16_store_row<32>(args, args.z, second, tl.group, row, col0);
+            }
+          } else {
+            // 64 bytes of each row at a time through the warp's staging tile
+            // (64-byte swizzle); a store must have read it before the next is written
+            auto put = [&](const CUtensorMap* map, const uint32_t* w, int x) {
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t off = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + off), "r"(w[4 * j]), "r"(w[4 * j + 1]),
+                             "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                             : "memory");
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(map, stg, x, row_w, args.mode == kRaggedM ? 0 : tl.group);
+                bulk_commit_group();
+              }
+            };
+            if (args.out_type == 2) {
+              uint32_t w[16];
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[p * 16 + j]);
+                if (col0 + p * 16 < args.n) put(&tmap_d, w, col0 + p * 16);
+              }
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
+              put(&tmap_d, w, col0);
+              if (EPI != kEpiPlain && args.z != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack16(second[2 * j], second[2 * j + 1], h);
+                put(&tmap_z, w, col0);
+              }
+            }
+          }
+          if (EPI == kEpiPoly && args.sym && tl.mb != tl.nb && valid) g16_store_mirror<32>(args, v, tl.group, row, col0);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(buf), 0));
+    }
+    if (lane == 0) bulk_wait_group_all();
+  }
+
+  // neither CTA may leave while its peer can still signal its barriers, read
+  // its shared memory or write its TMEM; a CTA that gave up lingers first
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (threadIdx.x == 0 && *abort_flag) linger_after_abort();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ======================================================================= one-CTA split-K kernel
+
+constexpr int kS16Stages = 3;
+constexpr int kS16Threads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kS16T = 128;        // tile rows and columns
+constexpr int kS16K = 64;
+
+struct S16Layout {
+  static constexpr int OP_BYTES = 128 * 128;  // 16 KB
+  static constexpr int OFF_A = 0;
+  static constexpr int OFF_B = OFF_A + kS16Stages * OP_BYTES;
+  static constexpr int OFF_BAR = OFF_B + kS16Stages * OP_BYTES;
+  static constexpr int NUM_BARS = 2 * kS16Stages + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_TAB = (OFF_MISC + 16 + 15) / 16 * 16;
+  static constexpr int BYTES = OFF_TAB + (kMaxGroups + 1) * 4;
+  static constexpr int ALLOC = BYTES + 1024;
+  // partial sums of the other CTAs (at most 7 slices of 16 columns x 128 rows,
+  // or 1 of 64) take the operand ring's place once the MMAs are done
+  static_assert(7 * 16 * 128 * 4 <= OFF_BAR && 64 * 128 * 4 <= OFF_BAR, "reduction buffer");
+  static_assert(2 * ALLOC <= 232448, "two CTAs to an SM");
+};
+
+template <int EPI>
+__global__ void __launch_bounds__(kS16Threads, 2)
+    g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const G16Args args) {
+  using L = S16Layout;
+  constexpr int S = kS16Stages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int splits = args.splits;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int part = static_cast<int>(blockIdx.x) - tile * splits;  // also the rank in the cluster
+
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile uint32_t* tmem_slot = misc + 0;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + L::OFF_TAB);
+  auto full_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * s; };
+  auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
+  const uint32_t acc_bar = sbase + L::OFF_BAR + 8u * (2 * S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(acc_bar, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmap_a);
+    prefetch_tmap(&tmap_b);
+  }
+  pdl_launch_dependents();
+  pdl_wait_prior();
+
+  int total;
+  if (args.mode == kRaggedM) {
+    const int bad = __syncthreads_or(g16_offsets_bad(args, args.m));
+    if (bad && threadIdx.x == 0 && blockIdx.x == 0) report(args.status, 0x1);
+    if (warp == 0) g16_prefix<kS16T>(args, tab, bad);
+    __syncthreads();
+    total = tab[args.groups];
+  } else {
+    total = args.groups * g16_tiles_per_entry(args);
+  }
+  if (tile >= total) return;  // the whole cluster has this tile (the grid covers the most tiles there can be)
+
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kS16T);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const G16Tile tl = g16_decode<kS16T>(args, tab, tile);
+  const int chunks = (args.k + kS16K - 1) / kS16K;
+  const int c_begin = static_cast<int>(static_cast<int64_t>(chunks) * part / splits);
+  const int c_end = static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / splits);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ===== TMA producer.  A K-major A comes in boxes of 32 rows, and only
+      // those with rows of the tile; the other rows of the tile are whatever the
+      // shared memory holds and feed accumulator rows that are never stored.
+      const int left = tl.rows_end - tl.row0;
+      const int a_boxes = args.a_mn ? 2 : ((left < kS16T ? left : kS16T) + 31) / 32;
+      const int a_z = args.mode == kBatched ? tl.group : 0;
+      const int b_z = args.b_per_group ? tl.group : 0;
+      const int col0 = tl.nb * kS16T;
+      const uint32_t bytes = (args.a_mn ? L::OP_BYTES : a_boxes * 4096) + L::OP_BYTES;
+      bool ok = true;
+      for (int c = c_begin; c < c_end; ++c) {
+        const int i = c - c_begin;
+        const int s = i % S;
+        if (!mbar_wait(empty_bar(s), ((i / S) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        mbar_arrive_expect_tx(full_bar(s), bytes);
+        const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
+        const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
+        const int kk = c * kS16K;
+        if (args.b_mn) {
+          tma_load_3d(sb, &tmap_b, full_bar(s), col0, kk, b_z);
+          tma_load_3d(sb + 8192, &tmap_b, full_bar(s), col0 + 64, kk, b_z);
+        } else {
+          tma_load_3d(sb, &tmap_b, full_bar(s), kk, col0, b_z);
+        }
+        if (args.a_mn) {
+          tma_load_3d(sa, &tmap_a, full_bar(s), tl.row0, kk, a_z);
+          tma_load_3d(sa + 8192, &tmap_a, full_bar(s), tl.row0 + 64, kk, a_z);
+        } else {
+          for (int b = 0; b < a_boxes; ++b) tma_load_3d(sa + b * 4096, &tmap_a, full_bar(s), kk, tl.row0 + b * 32, a_z);
+        }
+      }
+      if (!ok) {
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(kS16T, kS16T, args.op_fp16, args.a_mn, args.b_mn);
+      bool ok = true;
+      for (int c = c_begin; c < c_end; ++c) {
+        const int i = c - c_begin;
+        const int s = i % S;
+        if (!mbar_wait(full_bar(s), (i / S) & 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
+        const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
+        const int left = args.k - c * kS16K;
+#pragma unroll
+        for (int q = 0; q < kS16K / 16; ++q) {
+          if (q * 16 < left) {
+            const uint64_t da = args.a_mn ? desc_mnmajor_sw128(sa + q * 2048, 8192) : desc_kmajor_sw128(sa + q * 32);
+            const uint64_t db = args.b_mn ? desc_mnmajor_sw128(sb + q * 2048, 8192) : desc_kmajor_sw128(sb + q * 32);
+            tc_mma_f16(tmem_base, da, db, idesc, (i | q) != 0 ? 1u : 0u);
+          }
+        }
+        tc_commit(empty_bar(s));
+      }
+      if (!ok) {
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+      tc_commit(acc_bar);  // on every path, so that nothing is in flight when TMEM is freed
+      mbar_wait(acc_bar, 0, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  }
+  bool got = true;
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+  const int row = tl.row0 + r;
+  const bool valid = row < tl.rows_end;
+  if (warp >= 2) {
+    got = mbar_wait(acc_bar, 0, abort_flag, args.wait_ns);
+    got = __all_sync(0xFFFFFFFFu, got);
+    if (!got && lane == 0) {
+      report(args.status, 0x4);
+      *abort_flag = 1;
+    }
+    tc_fence_after();
+  }
+  const int width = kS16T / splits;  // columns of the tile this CTA finishes
+  if (splits > 1) {
+    // every CTA's MMAs have read their operands: the rings can take partial sums
+    cluster_sync();
+    if (warp >= 2 && got && tl.row0 + quarter * 32 < tl.rows_end) {
+      for (int o = 1; o < splits; ++o) {
+        const int owner = (part + o) % splits;
+        const int slot = part < owner ? part : part - 1;
+        const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>((slot * width * kS16T + r) * 4);
+#pragma unroll 1
+        for (int c = 0; c < width; c += 16) {
+          uint32_t raw[16];
+          tc_ld_32x32b_x16(t_row + owner * width + c, raw);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (c + j) * kS16T * 4), "r"(raw[j]) : "memory");
+        }
+      }
+    }
+    cluster_sync();
+  }
+  if (warp >= 2 && got && tl.row0 + quarter * 32 < tl.rows_end) {
+    const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+#pragma unroll 1
+    for (int c = 0; c < width; c += 16) {
+      const int col_t = part * width + c;
+      const int col0 = tl.nb * kS16T + col_t;
+      if (col0 >= args.n) break;
+      uint32_t raw[16];
+      tc_ld_32x32b_x16(t_row + col_t, raw);
+      tc_wait_ld();
+      float v[16], second[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
+      for (int slot = 0; slot < splits - 1; ++slot) {
+        const float* src = reinterpret_cast<const float*>(smem) + (slot * width + c) * kS16T + r;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += src[j * kS16T];
+      }
+      g16_epilogue<EPI, 16>(args, v, second, tl.group, row, col0, valid, scale);
+      if (valid) {
+        g16_store_row<16>(args, args.d, v, tl.group, row, col0);
+        if (EPI != kEpiPlain && args.z != nullptr) g16_store_row<16>(args, args.z, second, tl.group, row, col0);
+        if (EPI == kEpiPoly && args.sym && tl.mb != tl.nb) g16_store_mirror<16>(args, v, tl.group, row, col0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) linger_after_abort();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kS16T);
+  }
+}
+
+// ======================================================================= host
+
+// 16-bit operand [depth, rows, cols] (cols contiguous, rows `ld` elements
+// apart) read in boxes of box_rows x 64 elements, 128-byte swizzle.
+static bool make_tmap16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t depth, int64_t ld,
+                        int64_t batch, int box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(batch * 2)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// D (or z): boxes of 32 rows x 64 bytes, 64-byte swizzle (the epilogue's staging tiles).
+static bool make_tmap_out16(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t depth, int64_t ld,
+                            int64_t batch, bool fp32) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const int size = fp32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(batch * size)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / size), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The shared-memory attribute belongs to a kernel on a device: set once for each.
+constexpr int kMaxDevices = 64;
+template <typename K>
+static cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+static cudaLaunchConfig_t g16_config(int64_t ctas, int threads, int smem, int cluster, cudaStream_t stream,
+                                     cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int EPI>
+static cudaError_t launch_pair16(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
+                                 const CUtensorMap& tz, const G16Args& a, int64_t tiles, int num_sms,
+                                 cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = allow_smem(g16_pair_kernel<EPI>, P16Layout::ALLOC, done);
+  if (e != cudaSuccess) return e;
+  const int64_t most = num_sms / 2;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg =
+      g16_config(2 * (tiles < most ? tiles : most), kP16Threads, P16Layout::ALLOC, 2, stream, attr);
+  return cudaLaunchKernelEx(&cfg, g16_pair_kernel<EPI>, ta, tb, td, tz, a);
+}
+
+template <int EPI>
+static cudaError_t launch_small16(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
+                                  cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = allow_smem(g16_small_kernel<EPI>, S16Layout::ALLOC, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = g16_config(tiles * a.splits, kS16Threads, S16Layout::ALLOC, a.splits, stream, attr);
+  return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI>, ta, tb, a);
+}
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which kernel, and how many CTAs share a tile's K.  Time in units of one K
+// chunk of 64 on an SM: the pair kernel works through a 256 x 256 tile's chunk
+// in one unit on two SMs, the small kernel through a 128 x 128 tile's in about
+// one unit on one SM (its operands arrive no faster); a pass of the pair kernel
+// costs about 12 units more than its chunks, one of the small kernel 12, and a
+// split 6 for the exchange of partial sums.
+static bool pick_small(const Gemm16& p, int num_sms, int* splits) {
+  *splits = 1;
+  if (p.mode == kRaggedK) return false;  // the small kernel does not clear the rows behind a group
+  const int64_t chunks = ceil_div(p.k, kS16K);
+  int64_t mp, ms, entries = p.groups;
+  if (p.mode == kRaggedM) {  // the groups' sizes are on the device: all alike, to choose by
+    entries = p.m < p.groups ? p.m : p.groups;
+    mp = ceil_div(ceil_div(p.m, entries), kP16TM);
+    ms = ceil_div(ceil_div(p.m, entries), kS16T);
+  } else {
+    mp = ceil_div(p.m, kP16TM);
+    ms = ceil_div(p.m, kS16T);
+  }
+  const int64_t np = ceil_div(p.n, kP16TN), ns = ceil_div(p.n, kS16T);
+  const int64_t tiles_p = entries * (p.sym ? mp * (mp + 1) / 2 : mp * np);
+  const int64_t tiles_s = entries * (p.sym ? ms * (ms + 1) / 2 : ms * ns);
+  const int64_t cost_pair = ceil_div(tiles_p, num_sms / 2) * chunks + 12;
+  int64_t best = 0;
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > 1 && (chunks < 2 * s || tiles_s * s > 2 * num_sms)) break;
+    // two CTAs share an SM's feed
+    const int64_t cost = ceil_div(tiles_s * s, num_sms) * ceil_div(chunks, s) + 12 + (s > 1 ? 6 : 0);
+    if (best == 0 || cost < best) {
+      best = cost;
+      *splits = s;
+    }
+  }
+  return best < cost_pair;
+}
+
+cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
+  int splits = 1;
+  bool small = pick_small(p, num_sms, &splits);
+  // MX_GEMM16_CONFIG forces a kernel for tests and tuning: 0 the pair kernel, 1,
+  // 2, 4 or 8 the small one with that many CTAs (at most one per K chunk) a tile
+  if (const char* forced = std::getenv("MX_GEMM16_CONFIG")) {
+    const int v = std::atoi(forced);
+    if (v == 0) {
+      small = false;
+    } else if (p.mode != kRaggedK && (v == 1 || v == 2 || v == 4 || v == 8)) {
+      small = true;
+      for (splits = v; splits > ceil_div(p.k, kS16K); splits /= 2) {
+      }
+    }
+  }
+  const int tm = small ? kS16T : kP16TM, tn = small ? kS16T : kP16TN;
+
+  G16Args a = {};
+  a.bias = p.bias;
+  a.res = p.res;
+  a.res_lo = p.res_lo;
+  a.d = p.d;
+  a.z = p.z;
+  a.group_offsets = p.group_offsets;
+  a.scale = p.scale;
+  a.status = p.status;
+  a.wait_ns = wait_limit_ns();
+  a.d_ld = p.d_ld;
+  a.d_batch = p.mode == kRaggedM ? 0 : p.d_batch;  // ragged M: one D, its rows numbered through
+  a.res_ld = p.res_ld;
+  a.res_batch = p.res_batch;
+  a.alpha = p.alpha;
+  a.beta = p.beta;
+  a.diag = p.diag;
+  a.scale_pow = p.scale_pow;
+  a.m = static_cast<int>(p.m);
+  a.n = static_cast<int>(p.n);
+  a.k = static_cast<int>(p.k);
+  a.m_tiles = static_cast<int>(ceil_div(p.m, tm));
+  a.n_tiles = static_cast<int>(ceil_div(p.n, tn));
+  a.groups = static_cast<int>(p.groups);
+  a.mode = p.mode;
+  a.a_mn = p.a_mn;
+  a.b_mn = p.b_mn;
+  a.b_per_group = p.mode != kRaggedK;
+  a.op_fp16 = p.op_fp16;
+  a.out_type = p.out_type;
+  a.act = p.act;
+  a.sym = p.sym;
+  a.splits = splits;
+  a.tma_store = 1;
+
+  // the most tiles there can be (ragged M: every group adds at most one part tile a column)
+  const int64_t tiles = p.mode == kRaggedM ? (p.m / tm + p.groups) * a.n_tiles
+                                           : p.groups * (p.sym ? static_cast<int64_t>(a.m_tiles) * (a.m_tiles + 1) / 2
+                                                               : static_cast<int64_t>(a.m_tiles) * a.n_tiles);
+  if (tiles * splits > 0x3FFFFFFFll) return cudaErrorInvalidValue;  // tile numbers are 32-bit
+
+  const int64_t a_depth = p.mode == kBatched ? p.groups : 1;
+  const int64_t b_depth = a.b_per_group ? p.groups : 1;
+  const int box_a = small ? (p.a_mn ? 64 : 32) : 128;
+  const int box_b = small ? (p.b_mn ? 64 : 128) : 128;
+  CUtensorMap ta, tb, td = {}, tz = {};
+  if (!make_tmap16(&ta, p.a, p.a_mn ? p.m : p.k, p.a_mn ? p.k : p.m, a_depth, p.a_ld, p.a_batch, box_a) ||
+      !make_tmap16(&tb, p.b, p.b_mn ? p.n : p.k, p.b_mn ? p.k : p.n, b_depth, p.b_ld, p.b_batch, box_b))
+    return cudaErrorInvalidValue;
+  if (small) {
+    if (p.epi == kEpiLinear) return launch_small16<kEpiLinear>(ta, tb, a, tiles, stream);
+    if (p.epi == kEpiPoly) return launch_small16<kEpiPoly>(ta, tb, a, tiles, stream);
+    return launch_small16<kEpiPlain>(ta, tb, a, tiles, stream);
+  }
+  const int64_t d_depth = p.mode == kRaggedM ? 1 : p.groups;
+  if (!make_tmap_out16(&td, p.d, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2)) return cudaErrorInvalidValue;
+  if (p.z && !make_tmap_out16(&tz, p.z, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2))
+    return cudaErrorInvalidValue;
+  if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, a, tiles, num_sms, stream);
+  if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, a, tiles, num_sms, stream);
+  return launch_pair16<kEpiPlain>(ta, tb, td, tz, a, tiles, num_sms, stream);
+}
+
+}  // namespace mxk

@@ -1,0 +1,431 @@
+// mx_gemm16.cuh -- what the two kernels for 16-bit operands share (the
+// CTA-pair kernel for large products, the one-CTA split-K kernel for small
+// ones, both in mx_gemm16.cu): problem arguments, tile bookkeeping, operand
+// descriptors and the epilogue arithmetic.
+//
+//   D[i, j] = epilogue( sum_k A(i, k) * B(j, k) ),   BF16 or FP16 operands, FP32 sums
+//
+// Either operand may lie K-major ([rows, k], k contiguous) or MN-major
+// ([k, rows], rows contiguous): the weight gradient dW = dY^T X and the input
+// gradient dX = dY W read the tensors as the forward pass left them, without
+// a transposed copy.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "mx_gemm_common.cuh"
+#include "mx_launch.h"
+
+namespace mxk {
+
+// kRaggedM: group g owns rows [off[g], off[g+1]) of A and D, B is [groups, ...];
+// kRaggedK: group g owns that range of the reduction, D is [groups, m, n].
+enum G16Mode : int { kBatched = 0, kRaggedM = 1, kRaggedK = 2 };
+
+// kEpiPlain: D = acc.  kEpiLinear: z = acc + bias, D = act(z) + residual.
+// kEpiPoly: D = alpha * scale * acc + beta * (C + C_lo) + diag * I, with an
+// optional low half of D and, for a symmetric D, the mirrored tile.
+enum G16Epi : int { kEpiPlain = 0, kEpiLinear = 1, kEpiPoly = 2 };
+
+struct G16Args {
+  const void* bias;              // [n], operand type (linear)
+  const void* res;               // residual or C, rows as D's, pitch res_ld
+  const void* res_lo;            // low half of C (poly)
+  void* d;                       // out
+  void* z;                       // linear: pre-activation; poly: low half of D; null if not wanted
+  const int32_t* group_offsets;  // ragged forms
+  const float* scale;            // poly: factor per batch entry, raised to scale_pow (null: 1)
+  int32_t* status;
+  uint64_t wait_ns;
+  int64_t d_ld, res_ld;          // elements between rows
+  int64_t d_batch, res_batch;    // elements between batch entries
+  float alpha, beta, diag;
+  int scale_pow;
+  int m, n, k;                   // ragged M: m = all rows; ragged K: k = all rows
+  int m_tiles, n_tiles;          // of one batch entry (ragged M: n_tiles only)
+  int groups;                    // batch entries or groups
+  int mode;
+  int a_mn, b_mn;                // operand is MN-major
+  int b_per_group;               // B has a z coordinate (batched, ragged M)
+  int op_fp16;                   // operands are FP16 (else BF16); also the type of bias, residual, C
+  int out_type;                  // MX_BF16 / MX_FP16 / MX_FP32 of D and z
+  int act;
+  int sym;                       // D is symmetric: only tiles on and above the diagonal are computed
+  int tma_store;                 // D (and z) can be written by TMA
+  int splits;                    // one-CTA kernel: CTAs of a cluster that share one tile's K
+};
+
+// ---------------------------------------------------------------- tiles
+
+// Tiles of a grid of mt x nt: bands of 8 tile rows, down each column of a band
+// first, so that the tiles in flight at one time cover a nearly square piece of D
+// and share their operands' rows in L2.
+constexpr int kBand = 8;
+
+__device__ __forceinline__ void band_decode(int l, int mt, int nt, int& mb, int& nb) {
+  const int band = l / (kBand * nt);
+  const int m0 = band * kBand;
+  const int gm = mt - m0 < kBand ? mt - m0 : kBand;
+  const int r = l - m0 * nt;
+  nb = r / gm;
+  mb = m0 + r - nb * gm;
+}
+
+// Tile l of the upper triangle (mb <= nb), column by column: column nb has
+// nb + 1 tiles and starts at nb (nb + 1) / 2.
+__device__ __forceinline__ void tri_decode(int l, int& mb, int& nb) {
+  int c = static_cast<int>((sqrtf(8.0f * static_cast<float>(l) + 1.0f) - 1.0f) * 0.5f);
+  while (c * (c + 1) / 2 > l) --c;        // the square root may be off by one either way
+  while ((c + 1) * (c + 2) / 2 <= l) ++c;
+  nb = c;
+  mb = l - c * (c + 1) / 2;
+}
+
+__device__ __forceinline__ int g16_tiles_per_entry(const G16Args& a) {
+  return a.sym ? a.m_tiles * (a.m_tiles + 1) / 2 : a.m_tiles * a.n_tiles;
+}
+
+struct G16Tile {
+  int group;
+  int row0;      // first row of the tile (ragged M: of all rows)
+  int rows_end;  // rows at or beyond this are not the group's
+  int mb, nb;
+};
+
+// tab: exclusive prefix of row blocks (of TM rows) per group times n_tiles; ragged M only.
+template <int TM>
+__device__ __forceinline__ G16Tile g16_decode(const G16Args& a, const int32_t* tab, int t) {
+  G16Tile r;
+  if (a.mode == kRaggedM) {
+    r.group = last_le(tab, a.groups, t);
+    const int begin = __ldg(a.group_offsets + r.group);
+    r.rows_end = __ldg(a.group_offsets + r.group + 1);
+    band_decode(t - tab[r.group], (r.rows_end - begin + TM - 1) / TM, a.n_tiles, r.mb, r.nb);
+    r.row0 = begin + r.mb * TM;
+  } else {
+    const int per = g16_tiles_per_entry(a);
+    r.group = t / per;
+    const int l = t - r.group * per;
+    if (a.sym)
+      tri_decode(l, r.mb, r.nb);
+    else
+      band_decode(l, a.m_tiles, a.n_tiles, r.mb, r.nb);
+    r.row0 = r.mb * TM;
+    r.rows_end = a.m;
+  }
+  return r;
+}
+
+// First token and number of tokens of a group (ragged K), else all of K.
+__device__ __forceinline__ void g16_k_range(const G16Args& a, int group, int& k0, int& kn) {
+  if (a.mode == kRaggedK) {
+    k0 = __ldg(a.group_offsets + group);
+    kn = __ldg(a.group_offsets + group + 1) - k0;
+  } else {
+    k0 = 0;
+    kn = a.k;
+  }
+}
+
+// Offsets in order and inside [0, limit]?  (every thread a share of them)
+__device__ __forceinline__ int g16_offsets_bad(const G16Args& a, int limit) {
+  int bad = 0;
+  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x) {
+    const int32_t v = __ldg(a.group_offsets + i);
+    if (v < 0 || v > limit) bad = 1;
+    if (i > 0 && v < __ldg(a.group_offsets + i - 1)) bad = 1;
+  }
+  return bad;
+}
+
+// tab[g] = exclusive prefix over groups of ceil(rows / TM) * n_tiles (one warp).
+template <int TM>
+__device__ __forceinline__ void g16_prefix(const G16Args& a, int32_t* tab, int bad) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.groups + 31) / 32;
+  const int lo = lane * per;
+  auto tiles_of = [&](int e) -> int {
+    if (bad) return 0;
+    const int rows = __ldg(a.group_offsets + e + 1) - __ldg(a.group_offsets + e);
+    return (rows + TM - 1) / TM * a.n_tiles;
+  };
+  int sum = 0;
+  for (int i = lo; i < lo + per && i < a.groups; ++i) sum += tiles_of(i);
+  int incl = sum;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  int run = incl - sum;
+  for (int i = lo; i < lo + per && i < a.groups; ++i) {
+    tab[i] = run;
+    run += tiles_of(i);
+  }
+  if (lane == 31) tab[a.groups] = incl;
+}
+
+// ---------------------------------------------------------------- tensor core
+
+// Instruction descriptor for kind::f16 into FP32: both operands of one type;
+// bits 15 and 16 mark an MN-major A or B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fp16, int a_mn, int b_mn) {
+  return (1u << 4)                                    // D format F32
+         | (static_cast<uint32_t>(fp16 ? 0 : 1) << 7)   // A format F16 / BF16
+         | (static_cast<uint32_t>(fp16 ? 0 : 1) << 10)  // B format
+         | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// MN-major operand tile written by TMA with 128-byte swizzling: each K row
+// holds 64 elements (128 B), 8-row groups 1024 B apart; the next 64 elements
+// along MN lie chunk_bytes further.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t addr, uint32_t chunk_bytes) {
+  return smem_desc(addr, chunk_bytes, 1024, kSwizzle128B);
+}
+
+__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// mbar_wait whose success also acquires what other CTAs of the cluster released.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit_ns) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (abort != nullptr && *abort) return false;
+      if (global_timer_ns() - t0 > limit_ns) return false;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- 16-bit values
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int fp16) {
+  if (fp16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, int fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// v[0..8) += or = eight 16-bit values at p
+__device__ __forceinline__ void load8(const void* p, int fp16, float (&f)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+  const float2 a = unpack16(w.x, fp16), b = unpack16(w.y, fp16), c = unpack16(w.z, fp16), d = unpack16(w.w, fp16);
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
+}
+
+// ---------------------------------------------------------------- activations
+
+// The logistic function through the exponential of a non-positive number, so
+// that neither the exponential nor the quotient overflows.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  const float t = __expf(-fabsf(x));
+  const float r = __fdividef(1.0f, 1.0f + t);
+  return x >= 0.0f ? r : t * r;
+}
+
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// act(z); 0.5 (1 + tanh u) = sigmoid(2 u).  relu keeps a NaN.
+__device__ __forceinline__ float act_f32(float z, int act) {
+  switch (act) {
+    case 1: return z < 0.0f ? 0.0f : z;
+    case 2: return z * sigmoid_f32(z);
+    case 3: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case 4: return z * sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    default: return z;
+  }
+}
+
+// act'(z)
+__device__ __forceinline__ float act_grad_f32(float z, int act) {
+  switch (act) {
+    case 1: return z > 0.0f ? 1.0f : 0.0f;
+    case 2: {
+      const float p = sigmoid_f32(z);
+      return p * (1.0f + z * (1.0f - p));
+    }
+    case 3: return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+    case 4: {
+      const float p = sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
+      return p + z * p * (1.0f - p) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ float g16_scale(const G16Args& a, int group) {
+  if (a.scale == nullptr) return a.alpha;
+  const float s = __ldg(a.scale + group);
+  return a.scale_pow == 2 ? a.alpha * s * s : a.alpha * s;
+}
+
+// The epilogue's arithmetic on C consecutive columns from col0 of one row, in
+// place.  `second` receives what goes to z (linear: the pre-activation; poly:
+// left to the caller).  `valid`: the row is the group's; columns at or beyond
+// n hold values that are never stored.  scale: g16_scale of the tile's group.
+template <int EPI, int C>
+__device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], float (&second)[C], int group, int64_t row,
+                                             int col0, bool valid, float scale) {
+  if constexpr (EPI == kEpiLinear) {
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int g = 0; g < C / 8; ++g) {
+        if (col0 + g * 8 < a.n) {
+          float b[8];
+          load8(static_cast<const uint16_t*>(a.bias) + col0 + g * 8, a.op_fp16, b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
+        }
+      }
+    }
+    if (a.z != nullptr) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) second[j] = v[j];
+    }
+    if (a.act != 0) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], a.act);
+    }
+    if (a.res != nullptr && valid) {
+      const uint16_t* res = static_cast<const uint16_t*>(a.res) + row * a.res_ld + col0;
+#pragma unroll
+      for (int g = 0; g < C / 8; ++g) {
+        if (col0 + g * 8 < a.n) {
+          float b[8];
+          load8(res + g * 8, a.op_fp16, b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
+        }
+      }
+    }
+  } else if constexpr (EPI == kEpiPoly) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] *= scale;
+    if (a.res != nullptr && valid) {
+      const int64_t at = group * a.res_batch + row * a.res_ld + col0;
+      const float beta = a.scale != nullptr && a.scale_pow == 1 ? a.beta * __ldg(a.scale + group) : a.beta;
+#pragma unroll
+      for (int g = 0; g < C / 8; ++g) {
+        if (col0 + g * 8 < a.n) {
+          float b[8];
+          load8(static_cast<const uint16_t*>(a.res) + at + g * 8, a.op_fp16, b);
+          if (a.res_lo != nullptr) {
+            float l[8];
+            load8(static_cast<const uint16_t*>(a.res_lo) + at + g * 8, a.op_fp16, l);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] += l[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[g * 8 + j] = fmaf(beta, b[j], v[g * 8 + j]);
+        }
+      }
+    }
+    if (a.diag != 0.0f) {
+      const int64_t j = row - col0;
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (j == i) v[i] += a.diag;
+    }
+    if (a.z != nullptr) {  // what rounding the value to the output type leaves
+#pragma unroll
+      for (int j = 0; j < C; j += 2) {
+        const float2 h = unpack16(pack16(v[j], v[j + 1], a.out_type == 1), a.out_type == 1);
+        second[j] = v[j] - h.x;
+        second[j + 1] = v[j + 1] - h.y;
+      }
+    }
+  }
+}
+
+// C columns of one row to global memory, whole groups of 8 columns inside n
+// (rows are padded to a multiple of 8 elements).
+template <int C>
+__device__ __forceinline__ void g16_store_row(const G16Args& a, void* out, const float (&v)[C], int group, int64_t row,
+                                              int col0) {
+  const int64_t at = group * a.d_batch + row * a.d_ld + col0;
+#pragma unroll
+  for (int g = 0; g < C / 8; ++g) {
+    if (col0 + g * 8 < a.n) {
+      const float* p = v + g * 8;
+      if (a.out_type == 2) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + g * 8);
+        o[0] = make_float4(p[0], p[1], p[2], p[3]);
+        o[1] = make_float4(p[4], p[5], p[6], p[7]);
+      } else {
+        const int h = a.out_type == 1;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + g * 8) =
+            make_uint4(pack16(p[0], p[1], h), pack16(p[2], p[3], h), pack16(p[4], p[5], h), pack16(p[6], p[7], h));
+      }
+    }
+  }
+}
+
+// The mirrored half of a symmetric D (16-bit): column col0 + j of this row
+// becomes row col0 + j; a warp's 32 rows are 64 consecutive bytes there.
+template <int C>
+__device__ __forceinline__ void g16_store_mirror(const G16Args& a, const float (&v)[C], int group, int64_t row,
+                                                 int col0) {
+  uint16_t* out = static_cast<uint16_t*>(a.d) + group * a.d_batch + row;
+#pragma unroll
+  for (int j = 0; j < C; j += 2) {
+    const uint32_t w = pack16(v[j], v[j + 1], a.out_type == 1);
+    if (col0 + j < a.n) out[(col0 + j) * a.d_ld] = static_cast<uint16_t>(w & 0xFFFFu);
+    if (col0 + j + 1 < a.n) out[(col0 + j + 1) * a.d_ld] = static_cast<uint16_t>(w >> 16);
+  }
+}
+
+}  // namespace mxk

@@ -78,6 +78,54 @@ struct TwProblem {
 
 cudaError_t launch_gemm_tw(const TwProblem& p, int num_sms, cudaStream_t stream);
 
+// One product of 16-bit operands (mx_gemm16.cu).  Strides in elements.
+struct Gemm16 {
+  const void* a;                 // a_mn ? [k, m] : [m, k], rows a_ld apart
+  const void* b;                 // b_mn ? [k, n] : [n, k], rows b_ld apart
+  void* d;                       // [m, n], rows d_ld apart
+  int64_t a_ld, a_batch, b_ld, b_batch, d_ld, d_batch;
+  int64_t m, n, k, groups;       // ragged M: m = all rows; ragged K: k = all rows
+  int mode = 0;                  // 0 batched, 1 ragged M, 2 ragged K
+  int a_mn = 0, b_mn = 0;
+  int op_fp16 = 0;               // operands FP16 (else BF16)
+  int out_type = 0;              // 0 BF16, 1 FP16, 2 FP32
+  const int32_t* group_offsets = nullptr;  // ragged forms (device, groups + 1)
+  int32_t* status = nullptr;
+  int epi = 0;                   // 0 plain, 1 linear, 2 poly
+  void* z = nullptr;             // linear: pre-activation; poly: low half of D
+  const void* bias = nullptr;
+  const void* res = nullptr;     // linear: residual; poly: C
+  const void* res_lo = nullptr;
+  int64_t res_ld = 0, res_batch = 0;
+  int act = 0;
+  int sym = 0;                   // poly: D symmetric
+  float alpha = 1.0f, beta = 0.0f, diag = 0.0f;
+  const float* scale = nullptr;  // poly: device factor per batch entry
+  int scale_pow = 1;
+};
+cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream);
+
+// dz = dy * act'(z) and, with dbias, its column sums (mx_act.cu); partial:
+// act_backward_chunks(m) * n floats, needed with dbias.
+int64_t act_backward_chunks(int64_t m);
+cudaError_t launch_act_backward(const void* dy, const void* z, void* dz, void* dbias, float* partial, int64_t m,
+                                int64_t n, int act, int fp16, cudaStream_t stream);
+
+// Newton-Schulz orthogonalisation (mx_ortho.cu).
+struct OrthoProblem {
+  const void* g;        // [batch, m, n] BF16, or FP32
+  void* out;            // [batch, m, n] BF16
+  void* workspace;      // ns_workspace_bytes
+  int32_t* status;
+  const float* coeffs;  // host, 3 per step
+  int64_t batch, m, n;
+  int steps;
+  float eps;
+  bool fp32;
+};
+size_t ns_workspace_bytes(int64_t batch, int64_t m, int64_t n, bool fp32, int steps);
+cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_t stream);
+
 // MoE expert-layer data movement (mx_moe.cu).
 cudaError_t launch_moe_route(const int32_t* ids, int64_t n, int E, int pad, int32_t* counts, int32_t* offsets,
                              int32_t* row, int32_t* dropped, cudaStream_t stream);
