@@ -19,7 +19,6 @@ Function names match the C ABI:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -779,25 +778,45 @@ def mx_moe_combine_peer(y_ptrs: torch.Tensor, y_rows: int, n: int, src_rank: tor
 
 # ---------------------------------------------------------------- 16-bit products
 
-@contextlib.contextmanager
-def _launch_on(t: torch.Tensor, stream):
+class _launch_on:
     """The device of ``t`` and the stream the call runs on, both made current,
-    so that what the call allocates belongs to that stream."""
-    with torch.cuda.device(t.device):
+    so that what the call allocates belongs to that stream.  Where they are
+    already (the usual call) nothing is switched."""
+
+    __slots__ = ("contexts", "pointer")
+
+    def __init__(self, t: torch.Tensor, stream):
+        index = t.get_device()
+        self.contexts = ()
+        if stream is None and index == torch.cuda.current_device():
+            self.pointer = torch._C._cuda_getCurrentRawStream(index)
+            return
+        device = torch.cuda.device(index)
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
+            self.contexts = (device,)
+            self.pointer = torch._C._cuda_getCurrentRawStream(index)
             return
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device)
         if s.device != t.device:
             raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
-        with torch.cuda.stream(s):
-            yield s.cuda_stream
+        self.contexts = (device, torch.cuda.stream(s))
+        self.pointer = s.cuda_stream
+
+    def __enter__(self) -> int:
+        for c in self.contexts:
+            c.__enter__()
+        return self.pointer
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
 def _check16(t: torch.Tensor, name: str, shape, dtype, device):
     """A contiguous tensor of the given shape and type on the given device."""
-    _check(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _check(t, dtype, name)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
@@ -807,16 +826,20 @@ def _operand16(t: torch.Tensor, name: str, dims: int) -> torch.dtype:
     """The type of the operand that sets the call's type (BF16 or FP16)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    _check(t, t.dtype, name)
+    dt = t.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {dt}")
+    if not t.is_cuda or not t.is_contiguous():
+        _check(t, dt, name)
     if t.dim() != dims:
         raise ValueError(f"{name} must be {dims}-D")
-    return t.dtype
+    return dt
 
 
 def _status_on(dev_status, device):
-    if dev_status is not None and isinstance(dev_status, torch.Tensor) and dev_status.device != device:
+    if dev_status is None:
+        return None
+    if isinstance(dev_status, torch.Tensor) and dev_status.device != device:
         raise ValueError(f"dev_status is on {dev_status.device}, the tensors on {device}")
     return _status_arg(dev_status)
 
@@ -838,17 +861,19 @@ def mx_linear_act(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = 
     dt = _operand16(x, "x", 2)
     act = _activation(activation)
     m, k = x.shape
-    _operand16(w, "w", 2)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a 2-D torch.Tensor")
     n = w.shape[0]
     dev = x.device
     _check16(w, "w", (n, k), dt, dev)
+    for t, nm, shape in ((bias, "bias", (n,)), (residual, "residual", (m, n)), (z, "z", (m, n)), (y, "y", (m, n))):
+        if t is not None:
+            _check16(t, nm, shape, dt, dev)
     with _launch_on(x, stream) as s:
-        y = torch.empty((m, n), dtype=dt, device=dev) if y is None else y
+        if y is None:
+            y = x.new_empty((m, n))
         if return_z and z is None:
-            z = torch.empty((m, n), dtype=dt, device=dev)
-        for t, nm, shape in ((bias, "bias", (n,)), (residual, "residual", (m, n)), (z, "z", (m, n)), (y, "y", (m, n))):
-            if t is not None:
-                _check16(t, nm, shape, dt, dev)
+            z = x.new_empty((m, n))
         _raise(_lib.mx_linear_act(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(z), _ptr(y), m, n, k, _DTYPES[dt],
                                   act, _status_on(dev_status, dev), s), "mx_linear_act")
     return y if z is None else (y, z)

@@ -7,7 +7,7 @@
 //    (tcgen05.mma cta_group::2, 128 rows of A and of B in each CTA's shared
 //    memory), persistent, the accumulator double-buffered in TMEM so that the
 //    epilogue of one tile runs beside the MMAs of the next.
-//      warp 0      TMA producer (both CTAs): 128 elements of K per stage
+//      warp 0      TMA producer (both CTAs): 64 elements of K per stage
 //      warp 1      MMA issuer (leader), K = 16 per instruction
 //      warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
 //      warp 10     ragged K only (both CTAs): clears the rows of the stage that
@@ -30,25 +30,25 @@ namespace mxk {
 
 // ======================================================================= CTA-pair kernel
 
-constexpr int kP16Stages = 3;
+constexpr int kP16Stages = 6;
 constexpr int kP16EpiWarps = 8;
 constexpr int kP16Threads = 32 * (2 + kP16EpiWarps + 1);
 constexpr int kP16TM = 256, kP16TN = 256;
-constexpr int kP16K = 128;  // elements of K per stage
+constexpr int kP16K = 64;     // elements of K per stage
+constexpr int kP16Seg = 256;  // kEpiSum: K per partial sum
 
 struct P16Layout {
-  static constexpr int CHUNK = 128 * 128;           // 16 KB: 128 rows of 128 bytes
-  static constexpr int OP_BYTES = 2 * CHUNK;        // one operand's half tile of a stage
+  static constexpr int OP_BYTES = 128 * 128;        // 16 KB: one operand's half tile of a stage
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + kP16Stages * OP_BYTES;
   static constexpr int OFF_STG = OFF_B + kP16Stages * OP_BYTES;
-  static constexpr int STG_BYTES = 32 * 64;         // per epilogue warp: 32 rows of 64 bytes
+  static constexpr int STG_BYTES = 32 * 128;        // per epilogue warp: 32 rows of 128 bytes
   static constexpr int OFF_BAR = OFF_STG + kP16EpiWarps * STG_BYTES;
   // full, empty, ready per stage; accumulator full and empty (2 each); drain
   static constexpr int NUM_BARS = 3 * kP16Stages + 5;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = OFF_MISC + 16;
-  static constexpr int BYTES = OFF_TAB + (kMaxGroups + 1) * 4;
+  static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(OFF_STG % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
   static_assert(ALLOC <= 232448, "shared memory budget");
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
     bad = g16_offsets_bad(args, args.mode == kRaggedM ? args.m : args.k);
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0 && rank == 0) report(args.status, 0x1);
-    if (args.mode == kRaggedM && warp == 0) g16_prefix<kP16TM>(args, tab, bad);
+    if (args.mode == kRaggedM && warp == 0) g16_prefix<kP16TM>(args, tab, bad, &misc[2]);
   }
   __syncthreads();
   if (warp == 1) {
@@ -122,10 +122,12 @@ __global__ void __launch_bounds__(kP16Threads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = bad ? 0 : args.mode == kRaggedM ? tab[args.groups] : args.groups * g16_tiles_per_entry(args);
+  const int total = bad                      ? 0
+                    : args.mode == kRaggedM ? static_cast<int>(misc[2])
+                                            : args.groups * g16_tiles_per_entry(args);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ===== TMA producer.  Both CTAs' loads complete on the leader's full
       // barrier; with ragged K on the CTA's own, which its warp 10 waits for.
       int stage = 0;
@@ -140,37 +142,31 @@ __global__ void __launch_bounds__(kP16Threads, 1)
         int k0, kn;
         g16_k_range(args, tl.group, k0, kn);
         for (int kk = 0; kk < kn; kk += kP16K) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
-          // a K-major operand's second chunk of 64 is not needed when K ends before it
-          const int k_chunks = kn - kk > 64 ? 2 : 1;
-          const uint32_t bytes = (args.a_mn ? L::OP_BYTES : k_chunks * L::CHUNK) +
-                                 (args.b_mn ? L::OP_BYTES : k_chunks * L::CHUNK);
+          if (!wait16<false>(empty_bar(stage), phase ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
           const uint32_t fb = ragged_k ? full_bar(stage) : map_to_rank(full_bar(stage), 0);
           if (ragged_k)
-            mbar_arrive_expect_tx(full_bar(stage), bytes);
+            mbar_arrive_expect_tx(full_bar(stage), 2 * L::OP_BYTES);
           else if (rank == 0)
-            mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+            mbar_arrive_expect_tx(full_bar(stage), 4 * L::OP_BYTES);
           const uint32_t sa = sbase + L::OFF_A + stage * L::OP_BYTES;
           const uint32_t sb = sbase + L::OFF_B + stage * L::OP_BYTES;
           if (ragged_k) {  // both operands MN-major, completing on this CTA's barrier
             tma_load_3d(sa, &tmap_a, fb, a_mn0, k0 + kk, a_z);
-            tma_load_3d(sa + L::CHUNK, &tmap_a, fb, a_mn0 + 64, k0 + kk, a_z);
+            tma_load_3d(sa + 8192, &tmap_a, fb, a_mn0 + 64, k0 + kk, a_z);
             tma_load_3d(sb, &tmap_b, fb, b_mn0, k0 + kk, b_z);
-            tma_load_3d(sb + L::CHUNK, &tmap_b, fb, b_mn0 + 64, k0 + kk, b_z);
+            tma_load_3d(sb + 8192, &tmap_b, fb, b_mn0 + 64, k0 + kk, b_z);
           } else {
             if (args.a_mn) {
               tma_load_3d_pair(sa, &tmap_a, fb, a_mn0, kk, a_z);
-              tma_load_3d_pair(sa + L::CHUNK, &tmap_a, fb, a_mn0 + 64, kk, a_z);
+              tma_load_3d_pair(sa + 8192, &tmap_a, fb, a_mn0 + 64, kk, a_z);
             } else {
               tma_load_3d_pair(sa, &tmap_a, fb, kk, a_mn0, a_z);
-              if (k_chunks == 2) tma_load_3d_pair(sa + L::CHUNK, &tmap_a, fb, kk + 64, a_mn0, a_z);
             }
             if (args.b_mn) {
               tma_load_3d_pair(sb, &tmap_b, fb, b_mn0, kk, b_z);
-              tma_load_3d_pair(sb + L::CHUNK, &tmap_b, fb, b_mn0 + 64, kk, b_z);
+              tma_load_3d_pair(sb + 8192, &tmap_b, fb, b_mn0 + 64, kk, b_z);
             } else {
               tma_load_3d_pair(sb, &tmap_b, fb, kk, b_mn0, b_z);
-              if (k_chunks == 2) tma_load_3d_pair(sb + L::CHUNK, &tmap_b, fb, kk + 64, b_mn0, b_z);
             }
           }
           if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -182,42 +178,52 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ===== MMA issuer: up to 8 pair MMAs of K = 16 per stage
+    if (rank == 0 && elect_one()) {
+      // ===== MMA issuer: up to 4 pair MMAs of K = 16 per stage.  Accumulator
+      // buffer `it & 1` takes a tile's sum, or (kEpiSum) that of kP16Seg of its K.
       const uint32_t idesc = idesc_f16(kP16TM, kP16TN, args.op_fp16, args.a_mn, args.b_mn);
+      const uint64_t da0 = args.a_mn ? desc_mnmajor_sw128(sbase + L::OFF_A, 8192) : desc_kmajor_sw128(sbase + L::OFF_A);
+      const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
+      const uint64_t da_step = args.a_mn ? 128 : 2, db_step = args.b_mn ? 128 : 2;  // 16 of K, in 16-byte units
       int stage = 0;
       uint32_t phase = 0;
-      int it = 0;
+      uint32_t it = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs, ++it) {
-        const int buf = it & 1;
-        if (!mbar_wait_cluster(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t acc = tmem_base + buf * kP16TN;
+      for (int t = pair; t < total && ok; t += npairs) {
         int k0, kn;
         g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
-        for (int kk = 0; kk < kn; kk += kP16K) {
-          const bool got = ragged_k ? mbar_wait_cluster(ready_bar(stage), phase, abort_flag, args.wait_ns)
-                                    : mbar_wait(full_bar(stage), phase, abort_flag, args.wait_ns);
-          if (!got) { ok = false; break; }
+        int kk = 0;
+        do {
+          const uint32_t buf = it & 1u;
+          if (!wait16<true>(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = sbase + L::OFF_A + stage * L::OP_BYTES;
-          const uint32_t sb = sbase + L::OFF_B + stage * L::OP_BYTES;
-          const int left = kn - kk;
-#pragma unroll
-          for (int s = 0; s < kP16K / 16; ++s) {
-            if (s * 16 < left) {  // what is behind K's end is zeros or was not loaded
-              const uint32_t k_off = (s >> 2) * L::CHUNK + (s & 3) * 32;
-              const uint64_t da = args.a_mn ? desc_mnmajor_sw128(sa + s * 2048, L::CHUNK) : desc_kmajor_sw128(sa + k_off);
-              const uint64_t db = args.b_mn ? desc_mnmajor_sw128(sb + s * 2048, L::CHUNK) : desc_kmajor_sw128(sb + k_off);
-              tc_mma_pair_f16(acc, da, db, idesc, (kk | s) != 0 ? 1u : 0u);
+          const uint32_t acc = tmem_base + buf * kP16TN;
+          const int k_end = EPI == kEpiSum && kn - kk > kP16Seg ? kk + kP16Seg : kn;
+          uint32_t accumulate = 0;
+          for (; kk < k_end; kk += kP16K) {
+            const bool got = ragged_k ? wait16<true>(ready_bar(stage), phase, abort_flag, args.wait_ns)
+                                      : wait16<false>(full_bar(stage), phase, abort_flag, args.wait_ns);
+            if (!got) { ok = false; break; }
+            const uint64_t da = da0 + static_cast<uint64_t>(stage * (L::OP_BYTES >> 4));
+            const uint64_t db = db0 + static_cast<uint64_t>(stage * (L::OP_BYTES >> 4));
+            // what is behind K's end is zeros or not this group's: left out
+            const int steps = kn - kk >= kP16K ? 4 : (kn - kk + 15) >> 4;
+            if (steps == 4) {
+              tc_mma_pair_f16(acc, da, db, idesc, accumulate);
+              tc_mma_pair_f16(acc, da + da_step, db + db_step, idesc, 1);
+              tc_mma_pair_f16(acc, da + 2 * da_step, db + 2 * db_step, idesc, 1);
+              tc_mma_pair_f16(acc, da + 3 * da_step, db + 3 * db_step, idesc, 1);
+            } else {
+              for (int s = 0; s < steps; ++s) tc_mma_pair_f16(acc, da + s * da_step, db + s * db_step, idesc, s | accumulate);
             }
+            accumulate = 1;
+            tc_commit_pair_multicast(empty_bar(stage), 0x3);
+            if (++stage == S) { stage = 0; phase ^= 1u; }
           }
-          tc_commit_pair_multicast(empty_bar(stage), 0x3);
-          if (++stage == S) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) break;
-        tc_commit_pair_multicast(accf_bar(buf), 0x3);
+          if (!ok) break;
+          tc_commit_pair_multicast(accf_bar(buf), 0x3);
+          ++it;
+        } while (kk < kn);
       }
       if (!ok) {
         report(args.status, 0x4);
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       }
       // every pair MMA issued must finish before either CTA frees its TMEM
       tc_commit_pair_multicast(drain_bar, 0x1);
-      mbar_wait(drain_bar, 0, nullptr, 100000000ull);
+      wait16<false>(drain_bar, 0, nullptr, 100000000ull);
     }
   } else if (warp == 2 + kP16EpiWarps) {
     if (ragged_k) {
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
         int k0, kn;
         g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
         for (int kk = 0; kk < kn; kk += kP16K) {
-          ok = mbar_wait(full_bar(stage), phase, abort_flag, args.wait_ns);
+          ok = wait16<false>(full_bar(stage), phase, abort_flag, args.wait_ns);
           if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
           const int left = kn - kk;
           if (left < kP16K && (left & 15) != 0) {
@@ -247,8 +253,8 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             // 4 tiles (A's and B's two 64-column chunks) x rows x 8 pieces of 16 bytes
             for (int i = lane; i < 4 * rows * 8; i += 32) {
               const int piece = i & 7, row = (i >> 3) % rows, tile = (i >> 3) / rows;
-              const uint32_t at = sbase + (tile < 2 ? L::OFF_A : L::OFF_B) + stage * L::OP_BYTES +
-                                  (tile & 1) * L::CHUNK + (left + row) * 128 + piece * 16;
+              const uint32_t at = sbase + (tile < 2 ? L::OFF_A : L::OFF_B) + stage * L::OP_BYTES + (tile & 1) * 8192 +
+                                  (left + row) * 128 + piece * 16;
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
             }
             fence_proxy_async_smem();
@@ -270,92 +276,137 @@ __global__ void __launch_bounds__(kP16Threads, 1)
     const int half = ew >> 2;
     const uint32_t stg = sbase + L::OFF_STG + ew * L::STG_BYTES;
     const int h = args.out_type == 1;
-    int it = 0;
-    for (int t = pair; t < total; t += npairs, ++it) {
-      const int buf = it & 1;
-      const bool got = mbar_wait(accf_bar(buf), (it >> 1) & 1u, abort_flag, args.wait_ns);
+    uint32_t it = 0;
+    bool ok = true;
+    // 32 words of each of the warp's rows through its staging tile (128-byte
+    // swizzle); the store before must have read it
+    auto put = [&](const CUtensorMap* map, const uint32_t* w, int x, int y, int z) {
+      if (lane == 0) bulk_wait_group_read<0>();
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t off = lane * 128 + ((j ^ (lane & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + off), "r"(w[4 * j]), "r"(w[4 * j + 1]),
+                     "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(map, stg, x, y, z);
+        bulk_commit_group();
+      }
+    };
+    // the accumulator's next buffer is full; false (on every lane) if the wait ran out
+    auto wait_full = [&]() -> bool {
+      const bool got = wait16<false>(accf_bar(it & 1u), (it >> 1) & 1u, abort_flag, args.wait_ns);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         if (lane == 0) {
           report(args.status, 0x4);
           *abort_flag = 1;
         }
-        break;
+        return false;
       }
       tc_fence_after();
+      return true;
+    };
+    // this warp has read the buffer
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(it & 1u), 0));
+      ++it;
+    };
+    for (int t = pair; t < total && ok; t += npairs) {
       const G16Tile tl = g16_decode<kP16TM>(args, tab, t);
       int k0, kn;
       g16_k_range(args, tl.group, k0, kn);
       const int row_w = tl.row0 + 128 * static_cast<int>(rank) + 32 * quarter;  // the warp's first row
       const int row = row_w + lane;
+      const int col_w = tl.nb * kP16TN + half * 128;                            // and column
       const bool valid = row < tl.rows_end;
+      const bool mine = row_w < tl.rows_end && col_w < args.n;  // anything to store
       // TMA clips rows behind the tensor's last but not behind a group's
-      const bool tma = args.tma_store && (args.mode != kRaggedM || row_w + 32 <= tl.rows_end);
-      const uint32_t t_row = tmem_base + buf * kP16TN + (static_cast<uint32_t>(quarter * 32) << 16);
-      const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
-      if (row_w < tl.rows_end) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col_t = half * 128 + c * 32;
-          const int col0 = tl.nb * kP16TN + col_t;
-          if (col0 >= args.n) break;
-          uint32_t raw[32];
-          tc_ld_32x32b_x32(t_row + col_t, raw);
-          tc_wait_ld();
-          float v[32], second[32];
+      const bool tma = args.mode != kRaggedM || row_w + 32 <= tl.rows_end;
+      const int z_out = args.mode == kRaggedM ? 0 : tl.group;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+      if constexpr (EPI == kEpiSum) {
+        // FP32 sums over a long K: the tensor core's accumulator truncates, so each
+        // kP16Seg of K goes into one of its own, and these are added here, rounded
+        float sum[128];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = kn == 0 ? 0.0f : __uint_as_float(raw[j]);  // no MMA wrote an empty sum
-          g16_epilogue<EPI, 32>(args, v, second, tl.group, row, col0, valid, scale);
-          if (!tma) {
-            if (valid) {
-              g16_store_row<32>(args, args.d, v, tl.group, row, col0);
-              if (EPI != kEpiPlain && args.z != nullptr) g16_store_row<32>(args, args.z, second, tl.group, row, col0);
-            }
-          } else {
-            // 64 bytes of each row at a time through the warp's staging tile
-            // (64-byte swizzle); a store must have read it before the next is written
-            auto put = [&](const CUtensorMap* map, const uint32_t* w, int x) {
-              if (lane == 0) bulk_wait_group_read<0>();
-              __syncwarp();
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        for (int kk = 0; ok && (kk == 0 || kk < kn); kk += kP16Seg) {
+          ok = wait_full();
+          if (!ok) break;
+          if (kn > 0) {  // no MMA wrote an empty sum
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t off = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + off), "r"(w[4 * j]), "r"(w[4 * j + 1]),
-                             "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
-                             : "memory");
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(map, stg, x, row_w, args.mode == kRaggedM ? 0 : tl.group);
-                bulk_commit_group();
-              }
-            };
-            if (args.out_type == 2) {
-              uint32_t w[16];
+            for (int c = 0; c < 8; ++c) {
+              uint32_t raw[16];
+              tc_ld_32x32b_x16(t_row + (it & 1u) * kP16TN + c * 16, raw);
+              tc_wait_ld();
 #pragma unroll
-              for (int p = 0; p < 2; ++p) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(v[p * 16 + j]);
-                if (col0 + p * 16 < args.n) put(&tmap_d, w, col0 + p * 16);
-              }
-            } else {
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
-              put(&tmap_d, w, col0);
-              if (EPI != kEpiPlain && args.z != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack16(second[2 * j], second[2 * j + 1], h);
-                put(&tmap_z, w, col0);
-              }
+              for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(raw[j]);
             }
           }
-          if (EPI == kEpiPoly && args.sym && tl.mb != tl.nb && valid) g16_store_mirror<32>(args, v, tl.group, row, col0);
+          release();
+        }
+        if (!ok) break;
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (col_w + c * 32 < args.n)
+              put(&tmap_d, reinterpret_cast<const uint32_t*>(sum) + c * 32, col_w + c * 32, row_w, z_out);
+        }
+      } else {
+        ok = wait_full();
+        if (!ok) break;
+        const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          const int col0 = col_w + c;
+          if (!mine || col0 >= args.n) {
+            if (c == 64) release();
+            continue;
+          }
+          float v[64];
+          {
+            uint32_t raw[2][32];
+            tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw[0]);
+            tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c + 32, raw[1]);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j / 32][j % 32]);
+          }
+          if (c == 64) release();
+          if (kn == 0) {  // no MMA wrote an empty sum
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+          }
+          auto put64 = [&](const CUtensorMap* map) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
+            put(map, w, col0, row_w, z_out);
+          };
+          g16_epilogue<EPI, 64>(args, v, tl.group, row, col0, valid, scale);
+          if constexpr (EPI == kEpiLinear) {
+            if (args.z != nullptr) put64(&tmap_z);
+            g16_activate<64>(args, v, row, col0, valid);
+          }
+          if (tma)
+            put64(&tmap_d);
+          else if (valid)
+            g16_store_row<64>(args, args.d, v, tl.group, row, col0);
+          if constexpr (EPI == kEpiPoly) {
+            if (args.sym && tl.mb != tl.nb && valid) g16_store_mirror<64>(args, v, tl.group, row, col0);
+            if (args.z != nullptr) {
+              g16_remainder<64>(args, v);
+              put64(&tmap_z);
+            }
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce_bar(buf), 0));
     }
     if (lane == 0) bulk_wait_group_all();
   }
@@ -388,7 +439,7 @@ struct S16Layout {
   static constexpr int NUM_BARS = 2 * kS16Stages + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = (OFF_MISC + 16 + 15) / 16 * 16;
-  static constexpr int BYTES = OFF_TAB + (kMaxGroups + 1) * 4;
+  static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
   static constexpr int ALLOC = BYTES + 1024;
   // partial sums of the other CTAs (at most 7 slices of 16 columns x 128 rows,
   // or 1 of 64) take the operand ring's place once the MMAs are done
@@ -439,9 +490,9 @@ __global__ void __launch_bounds__(kS16Threads, 2)
   if (args.mode == kRaggedM) {
     const int bad = __syncthreads_or(g16_offsets_bad(args, args.m));
     if (bad && threadIdx.x == 0 && blockIdx.x == 0) report(args.status, 0x1);
-    if (warp == 0) g16_prefix<kS16T>(args, tab, bad);
+    if (warp == 0) g16_prefix<kS16T>(args, tab, bad, &misc[2]);
     __syncthreads();
-    total = tab[args.groups];
+    total = static_cast<int>(misc[2]);
   } else {
     total = args.groups * g16_tiles_per_entry(args);
   }
@@ -461,7 +512,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
   const int c_end = static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / splits);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ===== TMA producer.  A K-major A comes in boxes of 32 rows, and only
       // those with rows of the tile; the other rows of the tile are whatever the
       // shared memory holds and feed accumulator rows that are never stored.
@@ -475,7 +526,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       for (int c = c_begin; c < c_end; ++c) {
         const int i = c - c_begin;
         const int s = i % S;
-        if (!mbar_wait(empty_bar(s), ((i / S) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        if (!wait16<false>(empty_bar(s), ((i / S) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(full_bar(s), bytes);
         const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
         const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
@@ -499,25 +550,21 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = idesc_f16(kS16T, kS16T, args.op_fp16, args.a_mn, args.b_mn);
+      const uint64_t da0 = args.a_mn ? desc_mnmajor_sw128(sbase + L::OFF_A, 8192) : desc_kmajor_sw128(sbase + L::OFF_A);
+      const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
+      const uint64_t da_step = args.a_mn ? 128 : 2, db_step = args.b_mn ? 128 : 2;  // 16 of K, in 16-byte units
       bool ok = true;
       for (int c = c_begin; c < c_end; ++c) {
         const int i = c - c_begin;
         const int s = i % S;
-        if (!mbar_wait(full_bar(s), (i / S) & 1u, abort_flag, args.wait_ns)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
-        const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
+        if (!wait16<false>(full_bar(s), (i / S) & 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        const uint64_t da = da0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
+        const uint64_t db = db0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
         const int left = args.k - c * kS16K;
-#pragma unroll
-        for (int q = 0; q < kS16K / 16; ++q) {
-          if (q * 16 < left) {
-            const uint64_t da = args.a_mn ? desc_mnmajor_sw128(sa + q * 2048, 8192) : desc_kmajor_sw128(sa + q * 32);
-            const uint64_t db = args.b_mn ? desc_mnmajor_sw128(sb + q * 2048, 8192) : desc_kmajor_sw128(sb + q * 32);
-            tc_mma_f16(tmem_base, da, db, idesc, (i | q) != 0 ? 1u : 0u);
-          }
-        }
+        const int steps = left >= kS16K ? 4 : (left + 15) >> 4;  // zeros behind K's end are left out
+        for (int q = 0; q < steps; ++q) tc_mma_f16(tmem_base, da + q * da_step, db + q * db_step, idesc, (i | q) != 0 ? 1u : 0u);
         tc_commit(empty_bar(s));
       }
       if (!ok) {
@@ -525,7 +572,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
         *abort_flag = 1;
       }
       tc_commit(acc_bar);  // on every path, so that nothing is in flight when TMEM is freed
-      mbar_wait(acc_bar, 0, nullptr, 100000000ull);
+      wait16<false>(acc_bar, 0, nullptr, 100000000ull);
     }
     __syncwarp();
   }
@@ -536,7 +583,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
   const int row = tl.row0 + r;
   const bool valid = row < tl.rows_end;
   if (warp >= 2) {
-    got = mbar_wait(acc_bar, 0, abort_flag, args.wait_ns);
+    got = wait16<false>(acc_bar, 0, abort_flag, args.wait_ns);
     got = __all_sync(0xFFFFFFFFu, got);
     if (!got && lane == 0) {
       report(args.status, 0x4);
@@ -576,7 +623,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       uint32_t raw[16];
       tc_ld_32x32b_x16(t_row + col_t, raw);
       tc_wait_ld();
-      float v[16], second[16];
+      float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
       for (int slot = 0; slot < splits - 1; ++slot) {
@@ -584,11 +631,20 @@ __global__ void __launch_bounds__(kS16Threads, 2)
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] += src[j * kS16T];
       }
-      g16_epilogue<EPI, 16>(args, v, second, tl.group, row, col0, valid, scale);
+      g16_epilogue<EPI, 16>(args, v, tl.group, row, col0, valid, scale);
+      if constexpr (EPI == kEpiLinear) {
+        if (args.z != nullptr && valid) g16_store_row<16>(args, args.z, v, tl.group, row, col0);
+        g16_activate<16>(args, v, row, col0, valid);
+      }
       if (valid) {
         g16_store_row<16>(args, args.d, v, tl.group, row, col0);
-        if (EPI != kEpiPlain && args.z != nullptr) g16_store_row<16>(args, args.z, second, tl.group, row, col0);
-        if (EPI == kEpiPoly && args.sym && tl.mb != tl.nb) g16_store_mirror<16>(args, v, tl.group, row, col0);
+        if constexpr (EPI == kEpiPoly) {
+          if (args.sym && tl.mb != tl.nb) g16_store_mirror<16>(args, v, tl.group, row, col0);
+          if (args.z != nullptr) {
+            g16_remainder<16>(args, v);
+            g16_store_row<16>(args, args.z, v, tl.group, row, col0);
+          }
+        }
       }
     }
   }
@@ -620,7 +676,7 @@ static bool make_tmap16(CUtensorMap* m, const void* base, int64_t cols, int64_t 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// D (or z): boxes of 32 rows x 64 bytes, 64-byte swizzle (the epilogue's staging tiles).
+// D (or z): boxes of 32 rows x 128 bytes, 128-byte swizzle (the epilogue's staging tiles).
 static bool make_tmap_out16(CUtensorMap* m, void* base, int64_t cols, int64_t rows, int64_t depth, int64_t ld,
                             int64_t batch, bool fp32) {
   EncodeTiledFn enc = get_encode_fn();
@@ -629,10 +685,10 @@ static bool make_tmap_out16(CUtensorMap* m, void* base, int64_t cols, int64_t ro
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(depth)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * size), static_cast<cuuint64_t>(batch * size)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / size), 32, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -780,7 +836,6 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   a.act = p.act;
   a.sym = p.sym;
   a.splits = splits;
-  a.tma_store = 1;
 
   // the most tiles there can be (ragged M: every group adds at most one part tile a column)
   const int64_t tiles = p.mode == kRaggedM ? (p.m / tm + p.groups) * a.n_tiles
@@ -790,8 +845,8 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
 
   const int64_t a_depth = p.mode == kBatched ? p.groups : 1;
   const int64_t b_depth = a.b_per_group ? p.groups : 1;
-  const int box_a = small ? (p.a_mn ? 64 : 32) : 128;
-  const int box_b = small ? (p.b_mn ? 64 : 128) : 128;
+  const int box_a = p.a_mn ? 64 : small ? 32 : 128;
+  const int box_b = p.b_mn ? 64 : 128;
   CUtensorMap ta, tb, td = {}, tz = {};
   if (!make_tmap16(&ta, p.a, p.a_mn ? p.m : p.k, p.a_mn ? p.k : p.m, a_depth, p.a_ld, p.a_batch, box_a) ||
       !make_tmap16(&tb, p.b, p.b_mn ? p.n : p.k, p.b_mn ? p.k : p.n, b_depth, p.b_ld, p.b_batch, box_b))
@@ -805,6 +860,7 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   if (!make_tmap_out16(&td, p.d, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2)) return cudaErrorInvalidValue;
   if (p.z && !make_tmap_out16(&tz, p.z, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2))
     return cudaErrorInvalidValue;
+  if (p.out_type == 2) return launch_pair16<kEpiSum>(ta, tb, td, tz, a, tiles, num_sms, stream);
   if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, a, tiles, num_sms, stream);
   if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, a, tiles, num_sms, stream);
   return launch_pair16<kEpiPlain>(ta, tb, td, tz, a, tiles, num_sms, stream);

@@ -28,7 +28,8 @@ enum G16Mode : int { kBatched = 0, kRaggedM = 1, kRaggedK = 2 };
 // kEpiPlain: D = acc.  kEpiLinear: z = acc + bias, D = act(z) + residual.
 // kEpiPoly: D = alpha * scale * acc + beta * (C + C_lo) + diag * I, with an
 // optional low half of D and, for a symmetric D, the mirrored tile.
-enum G16Epi : int { kEpiPlain = 0, kEpiLinear = 1, kEpiPoly = 2 };
+// kEpiSum: D = acc in FP32 (pair kernel only).
+enum G16Epi : int { kEpiPlain = 0, kEpiLinear = 1, kEpiPoly = 2, kEpiSum = 3 };
 
 struct G16Args {
   const void* bias;              // [n], operand type (linear)
@@ -54,7 +55,6 @@ struct G16Args {
   int out_type;                  // MX_BF16 / MX_FP16 / MX_FP32 of D and z
   int act;
   int sym;                       // D is symmetric: only tiles on and above the diagonal are computed
-  int tma_store;                 // D (and z) can be written by TMA
   int splits;                    // one-CTA kernel: CTAs of a cluster that share one tile's K
 };
 
@@ -95,15 +95,26 @@ struct G16Tile {
   int mb, nb;
 };
 
-// tab: exclusive prefix of row blocks (of TM rows) per group times n_tiles; ragged M only.
+// Ragged M: tab[i] is the number of tiles before group i * kTabStep (every
+// kTabStep-th group only, for shared memory's sake; the rest is counted from the offsets).
+constexpr int kTabStep = 4;
+
+template <int TM>
+__device__ __forceinline__ int g16_group_tiles(const G16Args& a, int e) {
+  return (__ldg(a.group_offsets + e + 1) - __ldg(a.group_offsets + e) + TM - 1) / TM * a.n_tiles;
+}
+
 template <int TM>
 __device__ __forceinline__ G16Tile g16_decode(const G16Args& a, const int32_t* tab, int t) {
   G16Tile r;
   if (a.mode == kRaggedM) {
-    r.group = last_le(tab, a.groups, t);
+    const int i = last_le(tab, (a.groups - 1) / kTabStep, t);
+    int l = t - tab[i];
+    r.group = i * kTabStep;
+    for (int n; r.group + 1 < a.groups && l >= (n = g16_group_tiles<TM>(a, r.group)); ++r.group) l -= n;
     const int begin = __ldg(a.group_offsets + r.group);
     r.rows_end = __ldg(a.group_offsets + r.group + 1);
-    band_decode(t - tab[r.group], (r.rows_end - begin + TM - 1) / TM, a.n_tiles, r.mb, r.nb);
+    band_decode(l, (r.rows_end - begin + TM - 1) / TM, a.n_tiles, r.mb, r.nb);
     r.row0 = begin + r.mb * TM;
   } else {
     const int per = g16_tiles_per_entry(a);
@@ -141,30 +152,27 @@ __device__ __forceinline__ int g16_offsets_bad(const G16Args& a, int limit) {
   return bad;
 }
 
-// tab[g] = exclusive prefix over groups of ceil(rows / TM) * n_tiles (one warp).
+// Fills tab (see g16_decode) and *total, the number of all tiles (one warp).
 template <int TM>
-__device__ __forceinline__ void g16_prefix(const G16Args& a, int32_t* tab, int bad) {
+__device__ __forceinline__ void g16_prefix(const G16Args& a, int32_t* tab, int bad, uint32_t* total) {
   const int lane = threadIdx.x & 31;
-  const int per = (a.groups + 31) / 32;
+  const int per = ((a.groups + 31) / 32 + kTabStep - 1) / kTabStep * kTabStep;  // groups of a lane
   const int lo = lane * per;
-  auto tiles_of = [&](int e) -> int {
-    if (bad) return 0;
-    const int rows = __ldg(a.group_offsets + e + 1) - __ldg(a.group_offsets + e);
-    return (rows + TM - 1) / TM * a.n_tiles;
-  };
   int sum = 0;
-  for (int i = lo; i < lo + per && i < a.groups; ++i) sum += tiles_of(i);
+  if (!bad)
+    for (int i = lo; i < lo + per && i < a.groups; ++i) sum += g16_group_tiles<TM>(a, i);
   int incl = sum;
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xFFFFFFFFu, incl, off);
     if (lane >= off) incl += y;
   }
+  if (lane == 31) *total = static_cast<uint32_t>(incl);
+  if (bad) return;
   int run = incl - sum;
   for (int i = lo; i < lo + per && i < a.groups; ++i) {
-    tab[i] = run;
-    run += tiles_of(i);
+    if (i % kTabStep == 0) tab[i / kTabStep] = run;
+    run += g16_group_tiles<TM>(a, i);
   }
-  if (lane == 31) tab[a.groups] = incl;
 }
 
 // ---------------------------------------------------------------- tensor core
@@ -184,6 +192,17 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int fp16, int a_m
 // along MN lie chunk_bytes further.
 __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t addr, uint32_t chunk_bytes) {
   return smem_desc(addr, chunk_bytes, 1024, kSwizzle128B);
+}
+
+// One lane of a converged warp, chosen so that the compiler knows the code it
+// guards to be uniform: tcgen05 and TMA operands then stay in uniform registers.
+// (Under `lane == 0` every MMA's descriptors went through per-thread registers,
+// and the issuing thread, not the tensor cores, bounded the kernel: 8192^3 917 us
+// against 751 us, and 707 us with the descriptors advanced instead of rebuilt.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -216,27 +235,31 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
       : "memory");
 }
 
-// mbar_wait whose success also acquires what other CTAs of the cluster released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
-                                                  uint64_t limit_ns) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
+// Bounded wait for a phase of a barrier, with the meaning of mbar_wait.  The
+// clock is read only once 32 attempts have failed: reading it after the first,
+// as mbar_wait does, delays every wait of a pipeline in step (the producer's for
+// a free stage, the MMA issuer's for a full one) by that read.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait16(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 15u) == 0) {
+    uint32_t ok;
+    if constexpr (CLUSTER)  // success also acquires what other CTAs of the cluster released
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (ok) return true;
+    if ((it & 31u) == 0) {
       if (abort != nullptr && *abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) return false;
     }
   }
 }
@@ -314,12 +337,14 @@ __device__ __forceinline__ float g16_scale(const G16Args& a, int group) {
 }
 
 // The epilogue's arithmetic on C consecutive columns from col0 of one row, in
-// place.  `second` receives what goes to z (linear: the pre-activation; poly:
-// left to the caller).  `valid`: the row is the group's; columns at or beyond
-// n hold values that are never stored.  scale: g16_scale of the tile's group.
+// place.  `valid`: the row is the group's; columns at or beyond n hold values
+// that are never stored.
+//
+// First part.  Linear: the pre-activation acc + bias.  Poly: D itself; scale is
+// g16_scale of the tile's group.
 template <int EPI, int C>
-__device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], float (&second)[C], int group, int64_t row,
-                                             int col0, bool valid, float scale) {
+__device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], int group, int64_t row, int col0, bool valid,
+                                             float scale) {
   if constexpr (EPI == kEpiLinear) {
     if (a.bias != nullptr) {
 #pragma unroll
@@ -327,26 +352,6 @@ __device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], fl
         if (col0 + g * 8 < a.n) {
           float b[8];
           load8(static_cast<const uint16_t*>(a.bias) + col0 + g * 8, a.op_fp16, b);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
-        }
-      }
-    }
-    if (a.z != nullptr) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) second[j] = v[j];
-    }
-    if (a.act != 0) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], a.act);
-    }
-    if (a.res != nullptr && valid) {
-      const uint16_t* res = static_cast<const uint16_t*>(a.res) + row * a.res_ld + col0;
-#pragma unroll
-      for (int g = 0; g < C / 8; ++g) {
-        if (col0 + g * 8 < a.n) {
-          float b[8];
-          load8(res + g * 8, a.op_fp16, b);
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
         }
@@ -376,18 +381,60 @@ __device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], fl
     }
     if (a.diag != 0.0f) {
       const int64_t j = row - col0;
+      if (j >= 0 && j < C) {
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (j == i) v[i] += a.diag;
-    }
-    if (a.z != nullptr) {  // what rounding the value to the output type leaves
-#pragma unroll
-      for (int j = 0; j < C; j += 2) {
-        const float2 h = unpack16(pack16(v[j], v[j + 1], a.out_type == 1), a.out_type == 1);
-        second[j] = v[j] - h.x;
-        second[j + 1] = v[j + 1] - h.y;
+        for (int i = 0; i < C; ++i)
+          if (j == i) v[i] += a.diag;
       }
     }
+  }
+}
+
+// Second part of the linear epilogue: activation and residual.
+template <int C>
+__device__ __forceinline__ void g16_activate(const G16Args& a, float (&v)[C], int64_t row, int col0, bool valid) {
+  switch (a.act) {  // one loop for each, not a choice for each value
+    case 1:
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], 1);
+      break;
+    case 2:
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], 2);
+      break;
+    case 3:
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], 3);
+      break;
+    case 4:
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_f32(v[j], 4);
+      break;
+    default: break;
+  }
+  if (a.res != nullptr && valid) {
+    const uint16_t* res = static_cast<const uint16_t*>(a.res) + row * a.res_ld + col0;
+#pragma unroll
+    for (int g = 0; g < C / 8; ++g) {
+      if (col0 + g * 8 < a.n) {
+        float b[8];
+        load8(res + g * 8, a.op_fp16, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
+      }
+    }
+  }
+}
+
+// What rounding the values to the output type leaves.
+template <int C>
+__device__ __forceinline__ void g16_remainder(const G16Args& a, float (&v)[C]) {
+  const int h = a.out_type == 1;
+#pragma unroll
+  for (int j = 0; j < C; j += 2) {
+    const float2 r = unpack16(pack16(v[j], v[j + 1], h), h);
+    v[j] -= r.x;
+    v[j + 1] -= r.y;
   }
 }
 
