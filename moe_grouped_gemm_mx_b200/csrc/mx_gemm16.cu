@@ -44,8 +44,8 @@ struct P16Layout {
   static constexpr int OFF_STG = OFF_B + kP16Stages * OP_BYTES;
   static constexpr int STG_BYTES = 32 * 128;        // per epilogue warp: 32 rows of 128 bytes
   static constexpr int OFF_BAR = OFF_STG + kP16EpiWarps * STG_BYTES;
-  // full, empty, ready per stage; accumulator full and empty (2 each); drain
-  static constexpr int NUM_BARS = 3 * kP16Stages + 5;
+  // full, empty, tail landed, tail cleared per stage; accumulator full and empty (2 each); drain
+  static constexpr int NUM_BARS = 4 * kP16Stages + 5;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = OFF_MISC + 16;
   static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
@@ -78,16 +78,23 @@ __global__ void __launch_bounds__(kP16Threads, 1)
 
   auto full_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * s; };
   auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
-  auto ready_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (2 * S + s); };
-  auto accf_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (3 * S + b); };
-  auto acce_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (3 * S + 2 + b); };
-  const uint32_t drain_bar = sbase + L::OFF_BAR + 8u * (3 * S + 4);
+  auto tail_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (2 * S + s); };
+  auto ready_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (3 * S + s); };
+  auto accf_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (4 * S + b); };
+  auto acce_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (4 * S + 2 + b); };
+  const uint32_t drain_bar = sbase + L::OFF_BAR + 8u * (4 * S + 4);
+  // ragged K: does a stage with `left` of the group's K end inside an MMA's 16,
+  // so that the rows behind it have to be cleared?  Such a stage lands on each
+  // CTA's own tail barrier, its warp 10 clears the rows and arrives on the
+  // leader's ready barrier; every other stage goes straight to the MMA issuer.
+  auto needs_clearing = [&](int left) { return ragged_k && left < kP16K && (left & 15) != 0; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);   // one arrival that announces the bytes
       mbar_init(empty_bar(s), 1);  // the leader's commit, multicast to both CTAs
-      mbar_init(ready_bar(s), 2);  // ragged K: one arrival from each CTA's warp 10, on the leader
+      mbar_init(tail_bar(s), 1);
+      mbar_init(ready_bar(s), 2);  // one arrival from each CTA's warp 10, on the leader
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
@@ -129,10 +136,20 @@ __global__ void __launch_bounds__(kP16Threads, 1)
   if (warp == 0) {
     if (elect_one()) {
       // ===== TMA producer.  Both CTAs' loads complete on the leader's full
-      // barrier; with ragged K on the CTA's own, which its warp 10 waits for.
+      // barrier, or (needs_clearing) on the CTA's own tail barrier.
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      auto load = [&](const CUtensorMap* map, uint32_t dst, uint32_t bar, int mn_major, int wide, int mn, int k, int z) {
+        if (!mn_major) {
+          tma_load_3d_pair(dst, map, bar, k, mn, z);
+        } else if (wide) {
+          tma_load_4d_pair(dst, map, bar, 0, k, mn / 64, z);
+        } else {
+          tma_load_3d_pair(dst, map, bar, mn, k, z);
+          tma_load_3d_pair(dst + 8192, map, bar, mn + 64, k, z);
+        }
+      };
       for (int t = pair; t < total && ok; t += npairs) {
         const G16Tile tl = g16_decode<kP16TM>(args, tab, t);
         const int a_mn0 = tl.row0 + 128 * static_cast<int>(rank);
@@ -143,32 +160,16 @@ __global__ void __launch_bounds__(kP16Threads, 1)
         g16_k_range(args, tl.group, k0, kn);
         for (int kk = 0; kk < kn; kk += kP16K) {
           if (!wait16<false>(empty_bar(stage), phase ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
-          const uint32_t fb = ragged_k ? full_bar(stage) : map_to_rank(full_bar(stage), 0);
-          if (ragged_k)
-            mbar_arrive_expect_tx(full_bar(stage), 2 * L::OP_BYTES);
-          else if (rank == 0)
+          uint32_t bar = map_to_rank(full_bar(stage), 0);
+          if (needs_clearing(kn - kk)) {
+            bar = map_to_rank(tail_bar(stage), rank);
+            mbar_arrive_expect_tx(tail_bar(stage), 2 * L::OP_BYTES);
+            if (rank == 0) mbar_arrive(full_bar(stage));  // a phase that nobody waits for
+          } else if (rank == 0) {
             mbar_arrive_expect_tx(full_bar(stage), 4 * L::OP_BYTES);
-          const uint32_t sa = sbase + L::OFF_A + stage * L::OP_BYTES;
-          const uint32_t sb = sbase + L::OFF_B + stage * L::OP_BYTES;
-          if (ragged_k) {  // both operands MN-major, completing on this CTA's barrier
-            tma_load_3d(sa, &tmap_a, fb, a_mn0, k0 + kk, a_z);
-            tma_load_3d(sa + 8192, &tmap_a, fb, a_mn0 + 64, k0 + kk, a_z);
-            tma_load_3d(sb, &tmap_b, fb, b_mn0, k0 + kk, b_z);
-            tma_load_3d(sb + 8192, &tmap_b, fb, b_mn0 + 64, k0 + kk, b_z);
-          } else {
-            if (args.a_mn) {
-              tma_load_3d_pair(sa, &tmap_a, fb, a_mn0, kk, a_z);
-              tma_load_3d_pair(sa + 8192, &tmap_a, fb, a_mn0 + 64, kk, a_z);
-            } else {
-              tma_load_3d_pair(sa, &tmap_a, fb, kk, a_mn0, a_z);
-            }
-            if (args.b_mn) {
-              tma_load_3d_pair(sb, &tmap_b, fb, b_mn0, kk, b_z);
-              tma_load_3d_pair(sb + 8192, &tmap_b, fb, b_mn0 + 64, kk, b_z);
-            } else {
-              tma_load_3d_pair(sb, &tmap_b, fb, kk, b_mn0, b_z);
-            }
           }
+          load(&tmap_a, sbase + L::OFF_A + stage * L::OP_BYTES, bar, args.a_mn, args.a_wide, a_mn0, k0 + kk, a_z);
+          load(&tmap_b, sbase + L::OFF_B + stage * L::OP_BYTES, bar, args.b_mn, args.b_wide, b_mn0, k0 + kk, b_z);
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
       }
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
       const uint64_t da_step = args.a_mn ? 128 : 2, db_step = args.b_mn ? 128 : 2;  // 16 of K, in 16-byte units
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tail_phase = 0;  // tail_phase: a bit per stage
       uint32_t it = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
@@ -201,9 +202,13 @@ __global__ void __launch_bounds__(kP16Threads, 1)
           const int k_end = EPI == kEpiSum && kn - kk > kP16Seg ? kk + kP16Seg : kn;
           uint32_t accumulate = 0;
           for (; kk < k_end; kk += kP16K) {
-            const bool got = ragged_k ? wait16<true>(ready_bar(stage), phase, abort_flag, args.wait_ns)
-                                      : wait16<false>(full_bar(stage), phase, abort_flag, args.wait_ns);
-            if (!got) { ok = false; break; }
+            if (needs_clearing(kn - kk)) {
+              ok = wait16<true>(ready_bar(stage), (tail_phase >> stage) & 1u, abort_flag, args.wait_ns);
+              tail_phase ^= 1u << stage;
+            } else {
+              ok = wait16<false>(full_bar(stage), phase, abort_flag, args.wait_ns);
+            }
+            if (!ok) break;
             const uint64_t da = da0 + static_cast<uint64_t>(stage * (L::OP_BYTES >> 4));
             const uint64_t db = db0 + static_cast<uint64_t>(stage * (L::OP_BYTES >> 4));
             // what is behind K's end is zeros or not this group's: left out
@@ -238,31 +243,31 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       // ===== the K rows behind a group's last token belong to the next group:
       // cleared up to the end of the MMAs' last step of 16 in both operands, so
       // that whatever they hold (infinities included) adds nothing
-      int stage = 0;
-      uint32_t phase = 0;
+      uint32_t next = 0, tail_phase = 0;  // stage of the next tile's first; a phase bit per stage
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
         int k0, kn;
         g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
-        for (int kk = 0; kk < kn; kk += kP16K) {
-          ok = wait16<false>(full_bar(stage), phase, abort_flag, args.wait_ns);
-          if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-          const int left = kn - kk;
-          if (left < kP16K && (left & 15) != 0) {
-            const int rows = 16 - (left & 15);
-            // 4 tiles (A's and B's two 64-column chunks) x rows x 8 pieces of 16 bytes
-            for (int i = lane; i < 4 * rows * 8; i += 32) {
-              const int piece = i & 7, row = (i >> 3) % rows, tile = (i >> 3) / rows;
-              const uint32_t at = sbase + (tile < 2 ? L::OFF_A : L::OFF_B) + stage * L::OP_BYTES + (tile & 1) * 8192 +
-                                  (left + row) * 128 + piece * 16;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(ready_bar(stage), 0));
-          if (++stage == S) { stage = 0; phase ^= 1u; }
+        if (kn == 0) continue;
+        const uint32_t stages = static_cast<uint32_t>((kn + kP16K - 1) / kP16K);
+        const uint32_t stage = (next + stages - 1) % S;
+        next = (next + stages) % S;
+        const int left = kn - (static_cast<int>(stages) - 1) * kP16K;
+        if (!needs_clearing(left)) continue;
+        ok = wait16<false>(tail_bar(stage), (tail_phase >> stage) & 1u, abort_flag, args.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        tail_phase ^= 1u << stage;
+        const int rows = 16 - (left & 15);
+        // 4 tiles (A's and B's two chunks of 64 columns) x rows x 8 pieces of 16 bytes
+        for (int i = lane; i < 4 * rows * 8; i += 32) {
+          const int piece = i & 7, row = (i >> 3) % rows, tile = (i >> 3) / rows;
+          const uint32_t at = sbase + (tile < 2 ? L::OFF_A : L::OFF_B) + stage * L::OP_BYTES + (tile & 1) * 8192 +
+                              (left + row) * 128 + piece * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(ready_bar(stage), 0));
       }
       if (!ok && lane == 0) {
         report(args.status, 0x4);
@@ -531,17 +536,21 @@ __global__ void __launch_bounds__(kS16Threads, 2)
         const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
         const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
         const int kk = c * kS16K;
-        if (args.b_mn) {
+        if (!args.b_mn) {
+          tma_load_3d(sb, &tmap_b, full_bar(s), kk, col0, b_z);
+        } else if (args.b_wide) {
+          tma_load_4d(sb, &tmap_b, full_bar(s), 0, kk, col0 / 64, b_z);
+        } else {
           tma_load_3d(sb, &tmap_b, full_bar(s), col0, kk, b_z);
           tma_load_3d(sb + 8192, &tmap_b, full_bar(s), col0 + 64, kk, b_z);
-        } else {
-          tma_load_3d(sb, &tmap_b, full_bar(s), kk, col0, b_z);
         }
-        if (args.a_mn) {
+        if (!args.a_mn) {
+          for (int b = 0; b < a_boxes; ++b) tma_load_3d(sa + b * 4096, &tmap_a, full_bar(s), kk, tl.row0 + b * 32, a_z);
+        } else if (args.a_wide) {
+          tma_load_4d(sa, &tmap_a, full_bar(s), 0, kk, tl.row0 / 64, a_z);
+        } else {
           tma_load_3d(sa, &tmap_a, full_bar(s), tl.row0, kk, a_z);
           tma_load_3d(sa + 8192, &tmap_a, full_bar(s), tl.row0 + 64, kk, a_z);
-        } else {
-          for (int b = 0; b < a_boxes; ++b) tma_load_3d(sa + b * 4096, &tmap_a, full_bar(s), kk, tl.row0 + b * 32, a_z);
         }
       }
       if (!ok) {
@@ -674,6 +683,31 @@ static bool make_tmap16(CUtensorMap* m, const void* base, int64_t cols, int64_t 
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// MN-major operand whose rows are whole groups of 64 elements, viewed as
+// [depth, cols / 64, rows, 64]: one box of two groups brings 128 of MN by 64 of
+// K, the groups 8 KB apart as the MMA's descriptor wants them.  (With a part
+// group at the end it would read behind the tensor's last row: two plain boxes then.)
+static bool make_tmap16_wide(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t depth, int64_t ld,
+                             int64_t batch) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
+                              static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld * 2), 128, static_cast<cuuint64_t>(batch * 2)};
+  const cuuint32_t box[4] = {64, 64, 2, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One operand's map: K-major [rows, k] in boxes of box_rows, or MN-major [k, mn].
+static bool make_operand16(CUtensorMap* m, const void* base, int mn_major, int wide, int64_t mn, int64_t k, int64_t depth,
+                           int64_t ld, int64_t batch, int box_rows) {
+  if (!mn_major) return make_tmap16(m, base, k, mn, depth, ld, batch, box_rows);
+  return wide ? make_tmap16_wide(m, base, mn, k, depth, ld, batch) : make_tmap16(m, base, mn, k, depth, ld, batch, 64);
 }
 
 // D (or z): boxes of 32 rows x 128 bytes, 128-byte swizzle (the epilogue's staging tiles).
@@ -830,6 +864,8 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   a.mode = p.mode;
   a.a_mn = p.a_mn;
   a.b_mn = p.b_mn;
+  a.a_wide = p.a_mn && p.m % 64 == 0;
+  a.b_wide = p.b_mn && p.n % 64 == 0;
   a.b_per_group = p.mode != kRaggedK;
   a.op_fp16 = p.op_fp16;
   a.out_type = p.out_type;
@@ -845,11 +881,9 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
 
   const int64_t a_depth = p.mode == kBatched ? p.groups : 1;
   const int64_t b_depth = a.b_per_group ? p.groups : 1;
-  const int box_a = p.a_mn ? 64 : small ? 32 : 128;
-  const int box_b = p.b_mn ? 64 : 128;
   CUtensorMap ta, tb, td = {}, tz = {};
-  if (!make_tmap16(&ta, p.a, p.a_mn ? p.m : p.k, p.a_mn ? p.k : p.m, a_depth, p.a_ld, p.a_batch, box_a) ||
-      !make_tmap16(&tb, p.b, p.b_mn ? p.n : p.k, p.b_mn ? p.k : p.n, b_depth, p.b_ld, p.b_batch, box_b))
+  if (!make_operand16(&ta, p.a, p.a_mn, a.a_wide, p.m, p.k, a_depth, p.a_ld, p.a_batch, small ? 32 : 128) ||
+      !make_operand16(&tb, p.b, p.b_mn, a.b_wide, p.n, p.k, b_depth, p.b_ld, p.b_batch, 128))
     return cudaErrorInvalidValue;
   if (small) {
     if (p.epi == kEpiLinear) return launch_small16<kEpiLinear>(ta, tb, a, tiles, stream);

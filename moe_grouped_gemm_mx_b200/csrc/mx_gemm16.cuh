@@ -50,6 +50,7 @@ struct G16Args {
   int groups;                    // batch entries or groups
   int mode;
   int a_mn, b_mn;                // operand is MN-major
+  int a_wide, b_wide;            // MN-major, and one box brings 128 of MN (4-D tensor map)
   int b_per_group;               // B has a z coordinate (batched, ragged M)
   int op_fp16;                   // operands are FP16 (else BF16); also the type of bias, residual, C
   int out_type;                  // MX_BF16 / MX_FP16 / MX_FP32 of D and z
@@ -222,6 +223,16 @@ __device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc,
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 4-D tiled TMA load global -> shared, completing on this CTA's `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 
