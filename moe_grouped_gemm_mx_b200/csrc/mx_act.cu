@@ -6,7 +6,8 @@
 // One pass over dY and Z: each thread keeps eight columns (16-byte loads and
 // stores) over a chunk of rows and leaves their sums; a second small launch
 // adds the chunks' sums in order, so the result does not change from call to
-// call.  Bound by its bytes.
+// call (with one chunk, up to 1024 rows, the first writes the result).  A block
+// has 64 columns, 128 bytes of each row.  Bound by its bytes.
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -15,16 +16,16 @@
 
 namespace mxk {
 
-constexpr int kActCols = 256;  // columns of a block: 32 threads of 8
-constexpr int kActRows = 8;    // rows a block works on at one time
+constexpr int kActCols = 64;   // columns of a block: 8 threads of 8
+constexpr int kActRows = 32;   // rows a block works on at one time
 
 template <int ACT>
 __global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __restrict__ dy,
                                                            const uint16_t* __restrict__ z, uint16_t* __restrict__ dz,
-                                                           float* __restrict__ partial, int64_t m, int n, int64_t chunk,
-                                                           int fp16) {
+                                                           float* __restrict__ partial, uint16_t* __restrict__ dbias,
+                                                           int64_t m, int n, int64_t chunk, int fp16) {
   __shared__ float sums[kActRows][kActCols + 1];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
   const int col = blockIdx.x * kActCols + tx * 8;
   const int64_t r0 = blockIdx.y * chunk;
   const int64_t r1 = r0 + chunk < m ? r0 + chunk : m;
@@ -49,16 +50,19 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __res
       for (int j = 0; j < 8; ++j) s[j] += g[j];
     }
   }
-  if (partial == nullptr) return;
+  if (dbias == nullptr) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[ty][tx * 8 + j] = s[j];
   __syncthreads();
   const int c = blockIdx.x * kActCols + threadIdx.x;
-  if (c < n) {
+  if (threadIdx.x < kActCols && c < n) {
     float t = 0.0f;
 #pragma unroll
     for (int i = 0; i < kActRows; ++i) t += sums[i][threadIdx.x];
-    partial[static_cast<int64_t>(blockIdx.y) * n + c] = t;
+    if (gridDim.y == 1)
+      dbias[c] = static_cast<uint16_t>(pack16(t, 0.0f, fp16) & 0xFFFFu);
+    else
+      partial[static_cast<int64_t>(blockIdx.y) * n + c] = t;
   }
 }
 
@@ -93,9 +97,11 @@ static cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream
   return cfg;
 }
 
-// Chunks of rows: enough blocks for the GPU, at most 64 sums a column to add.
+// Chunks of rows: one of up to 1024 rows, else enough blocks for the GPU, at
+// most 64 sums a column to add.
 int64_t act_backward_chunks(int64_t m) {
-  const int64_t c = (m + 31) / 32;
+  if (m <= 1024) return 1;
+  const int64_t c = (m + 127) / 128;
   return c < 64 ? c : 64;
 }
 
@@ -110,18 +116,18 @@ cudaError_t launch_act_backward(const void* dy, const void* z, void* dz, void* d
   const uint16_t* y16 = static_cast<const uint16_t*>(dy);
   const uint16_t* z16 = static_cast<const uint16_t*>(z);
   uint16_t* d16 = static_cast<uint16_t*>(dz);
-  float* part = dbias ? partial : nullptr;
+  uint16_t* db = static_cast<uint16_t*>(dbias);
   cudaError_t e;
   switch (act) {
-    case 0: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<0>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
-    case 1: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<1>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
-    case 2: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<2>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
-    case 3: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<3>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
-    default: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<4>, y16, z16, d16, part, m, static_cast<int>(n), chunk, fp16); break;
+    case 0: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<0>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
+    case 1: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<1>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
+    case 2: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<2>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
+    case 3: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<3>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
+    default: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<4>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
   }
-  if (e != cudaSuccess || !dbias) return e;
+  if (e != cudaSuccess || !dbias || m <= chunk) return e;
   cfg = pdl_config(dim3(static_cast<unsigned>((n + 31) / 32), 1, 1), 256, stream, attr);
-  return cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(part), static_cast<uint16_t*>(dbias),
+  return cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(partial), db,
                             static_cast<int>(n), static_cast<int>((m + chunk - 1) / chunk), fp16);
 }
 

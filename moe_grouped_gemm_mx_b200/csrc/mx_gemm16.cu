@@ -20,6 +20,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 
@@ -35,7 +36,7 @@ constexpr int kP16EpiWarps = 8;
 constexpr int kP16Threads = 32 * (2 + kP16EpiWarps + 1);
 constexpr int kP16TM = 256, kP16TN = 256;
 constexpr int kP16K = 64;     // elements of K per stage
-constexpr int kP16Seg = 256;  // kEpiSum: K per partial sum
+constexpr int kP16Seg = 512;  // kEpiSum: K per partial sum
 
 struct P16Layout {
   static constexpr int OP_BYTES = 128 * 128;        // 16 KB: one operand's half tile of a stage
@@ -431,17 +432,19 @@ __global__ void __launch_bounds__(kP16Threads, 1)
 
 // ======================================================================= one-CTA split-K kernel
 
-constexpr int kS16Stages = 3;
 constexpr int kS16Threads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kS16T = 128;        // tile rows and columns
 constexpr int kS16K = 64;
 
+// STAGES: 3 where two CTAs share an SM, 6 where a CTA has one to itself (the
+// operands of as many K chunks in flight either way).
+template <int STAGES>
 struct S16Layout {
   static constexpr int OP_BYTES = 128 * 128;  // 16 KB
   static constexpr int OFF_A = 0;
-  static constexpr int OFF_B = OFF_A + kS16Stages * OP_BYTES;
-  static constexpr int OFF_BAR = OFF_B + kS16Stages * OP_BYTES;
-  static constexpr int NUM_BARS = 2 * kS16Stages + 1;
+  static constexpr int OFF_B = OFF_A + STAGES * OP_BYTES;
+  static constexpr int OFF_BAR = OFF_B + STAGES * OP_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = (OFF_MISC + 16 + 15) / 16 * 16;
   static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
@@ -449,15 +452,15 @@ struct S16Layout {
   // partial sums of the other CTAs (at most 7 slices of 16 columns x 128 rows,
   // or 1 of 64) take the operand ring's place once the MMAs are done
   static_assert(7 * 16 * 128 * 4 <= OFF_BAR && 64 * 128 * 4 <= OFF_BAR, "reduction buffer");
-  static_assert(2 * ALLOC <= 232448, "two CTAs to an SM");
+  static_assert((STAGES <= 3 ? 2 : 1) * ALLOC <= 232448, "shared memory budget");
 };
 
-template <int EPI>
-__global__ void __launch_bounds__(kS16Threads, 2)
+template <int EPI, int STAGES>
+__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
     g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const G16Args args) {
-  using L = S16Layout;
-  constexpr int S = kS16Stages;
+  using L = S16Layout<STAGES>;
+  constexpr int S = STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -527,11 +530,11 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       const int b_z = args.b_per_group ? tl.group : 0;
       const int col0 = tl.nb * kS16T;
       const uint32_t bytes = (args.a_mn ? L::OP_BYTES : a_boxes * 4096) + L::OP_BYTES;
+      int s = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int c = c_begin; c < c_end; ++c) {
-        const int i = c - c_begin;
-        const int s = i % S;
-        if (!wait16<false>(empty_bar(s), ((i / S) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        if (!wait16<false>(empty_bar(s), phase ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(full_bar(s), bytes);
         const uint32_t sa = sbase + L::OFF_A + s * L::OP_BYTES;
         const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
@@ -552,6 +555,7 @@ __global__ void __launch_bounds__(kS16Threads, 2)
           tma_load_3d(sa, &tmap_a, full_bar(s), tl.row0, kk, a_z);
           tma_load_3d(sa + 8192, &tmap_a, full_bar(s), tl.row0 + 64, kk, a_z);
         }
+        if (++s == S) { s = 0; phase ^= 1u; }
       }
       if (!ok) {
         report(args.status, 0x4);
@@ -564,17 +568,26 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       const uint64_t da0 = args.a_mn ? desc_mnmajor_sw128(sbase + L::OFF_A, 8192) : desc_kmajor_sw128(sbase + L::OFF_A);
       const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
       const uint64_t da_step = args.a_mn ? 128 : 2, db_step = args.b_mn ? 128 : 2;  // 16 of K, in 16-byte units
+      int s = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int c = c_begin; c < c_end; ++c) {
         const int i = c - c_begin;
-        const int s = i % S;
-        if (!wait16<false>(full_bar(s), (i / S) & 1u, abort_flag, args.wait_ns)) { ok = false; break; }
+        if (!wait16<false>(full_bar(s), phase, abort_flag, args.wait_ns)) { ok = false; break; }
         const uint64_t da = da0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
         const uint64_t db = db0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
         const int left = args.k - c * kS16K;
         const int steps = left >= kS16K ? 4 : (left + 15) >> 4;  // zeros behind K's end are left out
-        for (int q = 0; q < steps; ++q) tc_mma_f16(tmem_base, da + q * da_step, db + q * db_step, idesc, (i | q) != 0 ? 1u : 0u);
+        if (steps == 4) {
+          tc_mma_f16(tmem_base, da, db, idesc, i != 0 ? 1u : 0u);
+          tc_mma_f16(tmem_base, da + da_step, db + db_step, idesc, 1);
+          tc_mma_f16(tmem_base, da + 2 * da_step, db + 2 * db_step, idesc, 1);
+          tc_mma_f16(tmem_base, da + 3 * da_step, db + 3 * db_step, idesc, 1);
+        } else {
+          for (int q = 0; q < steps; ++q) tc_mma_f16(tmem_base, da + q * da_step, db + q * db_step, idesc, (i | q) != 0 ? 1u : 0u);
+        }
         tc_commit(empty_bar(s));
+        if (++s == S) { s = 0; phase ^= 1u; }
       }
       if (!ok) {
         report(args.status, 0x4);
@@ -608,15 +621,16 @@ __global__ void __launch_bounds__(kS16Threads, 2)
       for (int o = 1; o < splits; ++o) {
         const int owner = (part + o) % splits;
         const int slot = part < owner ? part : part - 1;
-        const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>((slot * width * kS16T + r) * 4);
+        // [slot][quad of columns][row] of float4: a warp's 32 rows are 512 bytes
+        const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>((slot * (width / 4) * kS16T + r) * 16);
 #pragma unroll 1
         for (int c = 0; c < width; c += 16) {
           uint32_t raw[16];
           tc_ld_32x32b_x16(t_row + owner * width + c, raw);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (c + j) * kS16T * 4), "r"(raw[j]) : "memory");
+          for (int j = 0; j < 4; ++j)
+            st_cluster_v4(dst + (c / 4 + j) * kS16T * 16, raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
         }
       }
     }
@@ -636,9 +650,15 @@ __global__ void __launch_bounds__(kS16Threads, 2)
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
       for (int slot = 0; slot < splits - 1; ++slot) {
-        const float* src = reinterpret_cast<const float*>(smem) + (slot * width + c) * kS16T + r;
+        const float4* src = reinterpret_cast<const float4*>(smem) + ((slot * width + c) / 4) * kS16T + r;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += src[j * kS16T];
+        for (int j = 0; j < 4; ++j) {
+          const float4 f = src[j * kS16T];
+          v[4 * j] += f.x;
+          v[4 * j + 1] += f.y;
+          v[4 * j + 2] += f.z;
+          v[4 * j + 3] += f.w;
+        }
       }
       g16_epilogue<EPI, 16>(args, v, tl.group, row, col0, valid, scale);
       if constexpr (EPI == kEpiLinear) {
@@ -771,48 +791,89 @@ static cudaError_t launch_pair16(const CUtensorMap& ta, const CUtensorMap& tb, c
   return cudaLaunchKernelEx(&cfg, g16_pair_kernel<EPI>, ta, tb, td, tz, a);
 }
 
-template <int EPI>
-static cudaError_t launch_small16(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
-                                  cudaStream_t stream) {
+// Clusters of `splits` CTAs that the GPU holds at once with one CTA to an SM
+// (a cluster stays inside a GPC, so fewer than SMs / splits).
+static int64_t lone_clusters(int splits, int num_sms) {
+  static std::atomic<int> known[kMaxDevices][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 0;
+  int v = known[dev][splits].load(std::memory_order_relaxed);
+  if (v == 0) {
+    static std::atomic<bool> done[kMaxDevices];
+    if (allow_smem(g16_small_kernel<kEpiPlain, 6>, S16Layout<6>::ALLOC, done) != cudaSuccess) return 0;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = g16_config(splits, kS16Threads, S16Layout<6>::ALLOC, splits, nullptr, attr);
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&v, g16_small_kernel<kEpiPlain, 6>, &cfg) != cudaSuccess || v <= 0) {
+      cudaGetLastError();
+      v = num_sms / splits / 2;
+    }
+    known[dev][splits].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+template <int EPI, int STAGES>
+static cudaError_t launch_small16s(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
+                                   cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow_smem(g16_small_kernel<EPI>, S16Layout::ALLOC, done);
+  cudaError_t e = allow_smem(g16_small_kernel<EPI, STAGES>, S16Layout<STAGES>::ALLOC, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = g16_config(tiles * a.splits, kS16Threads, S16Layout::ALLOC, a.splits, stream, attr);
-  return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI>, ta, tb, a);
+  cudaLaunchConfig_t cfg =
+      g16_config(tiles * a.splits, kS16Threads, S16Layout<STAGES>::ALLOC, a.splits, stream, attr);
+  return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI, STAGES>, ta, tb, a);
+}
+
+template <int EPI>
+static cudaError_t launch_small16(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
+                                  int num_sms, cudaStream_t stream) {
+  return tiles <= lone_clusters(a.splits, num_sms) ? launch_small16s<EPI, 6>(ta, tb, a, tiles, stream)
+                                                   : launch_small16s<EPI, 3>(ta, tb, a, tiles, stream);
 }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Which kernel, and how many CTAs share a tile's K.  Time in units of one K
-// chunk of 64 on an SM: the pair kernel works through a 256 x 256 tile's chunk
-// in one unit on two SMs, the small kernel through a 128 x 128 tile's in about
-// one unit on one SM (its operands arrive no faster); a pass of the pair kernel
-// costs about 12 units more than its chunks, one of the small kernel 12, and a
-// split 6 for the exchange of partial sums.
+// Which kernel, and how many CTAs share a tile's K: the one whose estimated time
+// (in us, fitted to measured launches) is less.
+//   pair kernel: 8 us for launch, first operands and last epilogue, and 0.3 us per
+//     K chunk of 64 for each round of tiles (4096x1024x1024 12.8 us estimated, 12.9
+//     measured; 1037x7168x2048 27.2, 28.4; 64x2112x7168 42, 38.5).
+//   small kernel: 4 us, the exchange of partial sums, and per K chunk of a CTA
+//     0.25 us where it has an SM to itself (six stages), 0.39 us with three stages,
+//     0.51 us where two share one; the first six chunks 0.15 us more each, and
+//     2.5 us for every further round (64x2112x7168 by 4: 12.9 estimated, 12.9
+//     measured; by 2: 19.5, 19.7; 1037x7168x2048 whole: 42, 38.7).
 static bool pick_small(const Gemm16& p, int num_sms, int* splits) {
   *splits = 1;
-  if (p.mode == kRaggedK) return false;  // the small kernel does not clear the rows behind a group
+  if (p.mode == kRaggedK || p.out_type == 2) return false;  // neither clears rows behind a group nor sums in parts
   const int64_t chunks = ceil_div(p.k, kS16K);
-  int64_t mp, ms, entries = p.groups;
-  if (p.mode == kRaggedM) {  // the groups' sizes are on the device: all alike, to choose by
-    entries = p.m < p.groups ? p.m : p.groups;
-    mp = ceil_div(ceil_div(p.m, entries), kP16TM);
-    ms = ceil_div(ceil_div(p.m, entries), kS16T);
+  const double np = static_cast<double>(ceil_div(p.n, kP16TN)), ns = static_cast<double>(ceil_div(p.n, kS16T));
+  double tiles_p, tiles_s;
+  if (p.mode == kRaggedM) {
+    // the groups' sizes are on the device: the mean size, with half a tile more for each group's end
+    const double groups = static_cast<double>(p.m < p.groups ? p.m : p.groups), rows = static_cast<double>(p.m) / groups;
+    tiles_p = groups * std::fmax(1.0, rows / kP16TM + 0.5) * np;
+    tiles_s = groups * std::fmax(1.0, rows / kS16T + 0.5) * ns;
   } else {
-    mp = ceil_div(p.m, kP16TM);
-    ms = ceil_div(p.m, kS16T);
+    const double entries = static_cast<double>(p.groups);
+    const double mp = static_cast<double>(ceil_div(p.m, kP16TM)), ms = static_cast<double>(ceil_div(p.m, kS16T));
+    tiles_p = entries * (p.sym ? mp * (mp + 1) / 2 : mp * np);
+    tiles_s = entries * (p.sym ? ms * (ms + 1) / 2 : ms * ns);
   }
-  const int64_t np = ceil_div(p.n, kP16TN), ns = ceil_div(p.n, kS16T);
-  const int64_t tiles_p = entries * (p.sym ? mp * (mp + 1) / 2 : mp * np);
-  const int64_t tiles_s = entries * (p.sym ? ms * (ms + 1) / 2 : ms * ns);
-  const int64_t cost_pair = ceil_div(tiles_p, num_sms / 2) * chunks + 12;
-  int64_t best = 0;
+  const double cost_pair = 8.0 + 0.3 * std::ceil(tiles_p / (num_sms / 2)) * static_cast<double>(chunks);
+  double best = 1e30;
   for (int s = 1; s <= 8; s *= 2) {
-    if (s > 1 && (chunks < 2 * s || tiles_s * s > 2 * num_sms)) break;
-    // two CTAs share an SM's feed
-    const int64_t cost = ceil_div(tiles_s * s, num_sms) * ceil_div(chunks, s) + 12 + (s > 1 ? 6 : 0);
-    if (best == 0 || cost < best) {
+    if (s > chunks || (s > 1 && tiles_s * s > 2.0 * num_sms)) break;
+    const double each = static_cast<double>(ceil_div(chunks, s));
+    const double exchange = s == 1 ? 0.0 : s == 2 ? 0.6 : s == 4 ? 1.0 : 1.3 + 0.2 * tiles_s;
+    const double rounds = std::ceil(tiles_s * s / (2.0 * num_sms));
+    double cost = 4.0 + exchange + 0.15 * std::fmin(each, 6.0);
+    if (tiles_s <= static_cast<double>(lone_clusters(s, num_sms)))
+      cost += 0.25 * each;
+    else
+      cost += (tiles_s * s <= num_sms ? 0.39 : 0.51) * each * rounds + 2.5 * (rounds - 1.0);
+    if (cost < best) {
       best = cost;
       *splits = s;
     }
@@ -829,7 +890,7 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
     const int v = std::atoi(forced);
     if (v == 0) {
       small = false;
-    } else if (p.mode != kRaggedK && (v == 1 || v == 2 || v == 4 || v == 8)) {
+    } else if (p.mode != kRaggedK && p.out_type != 2 && (v == 1 || v == 2 || v == 4 || v == 8)) {
       small = true;
       for (splits = v; splits > ceil_div(p.k, kS16K); splits /= 2) {
       }
@@ -886,9 +947,9 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
       !make_operand16(&tb, p.b, p.b_mn, a.b_wide, p.n, p.k, b_depth, p.b_ld, p.b_batch, 128))
     return cudaErrorInvalidValue;
   if (small) {
-    if (p.epi == kEpiLinear) return launch_small16<kEpiLinear>(ta, tb, a, tiles, stream);
-    if (p.epi == kEpiPoly) return launch_small16<kEpiPoly>(ta, tb, a, tiles, stream);
-    return launch_small16<kEpiPlain>(ta, tb, a, tiles, stream);
+    if (p.epi == kEpiLinear) return launch_small16<kEpiLinear>(ta, tb, a, tiles, num_sms, stream);
+    if (p.epi == kEpiPoly) return launch_small16<kEpiPoly>(ta, tb, a, tiles, num_sms, stream);
+    return launch_small16<kEpiPlain>(ta, tb, a, tiles, num_sms, stream);
   }
   const int64_t d_depth = p.mode == kRaggedM ? 1 : p.groups;
   if (!make_tmap_out16(&td, p.d, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2)) return cudaErrorInvalidValue;

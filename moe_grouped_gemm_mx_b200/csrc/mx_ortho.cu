@@ -27,7 +27,7 @@
 
 namespace mxk {
 
-constexpr int kNormParts = 64;  // partial sums of squares per matrix
+constexpr int kNormParts = 256; // partial sums of squares per matrix
 constexpr int kLogSA = 12;      // A and B are held times 2^12
 
 // Sum of squares of a share of each matrix, in 64 bits: no square of an FP32

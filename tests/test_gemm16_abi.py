@@ -35,7 +35,7 @@ def test_linear_act(lib):
 def test_linear_act_backward(lib):
     ws = lib.mx_linear_act_backward_workspace_bytes
     assert ws(0, 8) == ws(8, 0) == ws(-1, 8) == 0
-    assert ws(1, 8) == 32 and ws(8192, 4096) == 64 * 4096 * 4
+    assert ws(1, 8) == ws(1024, 8) == 32 and ws(1025, 8) == 9 * 32 and ws(8192, 4096) == 64 * 4096 * 4
 
     def f(dy=FAKE, z=FAKE, x=FAKE, w=FAKE, dz=FAKE, dx=FAKE, dw=FAKE, db=FAKE, m=4, n=16, k=32, dtype=BF16, act=1, work=FAKE,
           size=1 << 20):
