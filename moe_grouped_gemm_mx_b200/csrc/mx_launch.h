@@ -125,6 +125,9 @@ struct OrthoProblem {
 };
 size_t ns_workspace_bytes(int64_t batch, int64_t m, int64_t n, bool fp32, int steps);
 cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_t stream);
+// The one-launch form for a short side of at most 128 (mx_ortho_small.cu);
+// *taken tells whether the matrix fits it and it was launched.
+cudaError_t launch_orthogonalize_small(const OrthoProblem& q, bool* taken, int num_sms, cudaStream_t stream);
 
 // MoE expert-layer data movement (mx_moe.cu).
 cudaError_t launch_moe_route(const int32_t* ids, int64_t n, int E, int pad, int32_t* counts, int32_t* offsets,

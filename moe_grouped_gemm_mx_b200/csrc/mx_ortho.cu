@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 #include "mx_gemm16.cuh"
 #include "mx_launch.h"
@@ -193,6 +195,12 @@ static cudaError_t launch_pdl(K kernel, dim3 grid, cudaStream_t stream, Args... 
 }
 
 cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_t stream) {
+  const char* forced = std::getenv("MX_ORTHO_CONFIG");  // "general": this path for every size (tests, tuning)
+  if (forced == nullptr || std::strcmp(forced, "general") != 0) {
+    bool taken = false;
+    const cudaError_t e = launch_orthogonalize_small(q, &taken, num_sms, stream);
+    if (e != cudaSuccess || taken) return e;
+  }
   const NsPlan p = ns_plan(q.batch, q.m, q.n, q.fp32, q.steps);
   uint8_t* ws = static_cast<uint8_t*>(q.workspace);
   double* part = reinterpret_cast<double*>(ws + p.part);

@@ -1,0 +1,500 @@
+// mx_ortho_small.cu -- Newton-Schulz orthogonalisation of matrices with at most
+// 128 rows (or columns) in one launch: a cluster of up to 16 CTAs holds a matrix
+// on chip from its first read to its last write.
+//
+// The general path (mx_ortho.cu) launches three products a step; on a matrix of
+// 32 x 7168 each is a few microseconds of launch, fill and drain around almost no
+// work.  Here, with r the short side and the long side in slices of `slice`
+// columns, CTA by CTA:
+//   X     FP32 in TMEM (lane = row, times 2^(sx + 12)), so that a X is exact to
+//         FP32, and as FP16 (times 2^sx) in shared memory for the products;
+//   A     each CTA multiplies its slice's X X^T (K = slice), the partial sums meet in
+//         distributed shared memory, each CTA adds some columns (in rank order), and
+//         everyone receives all of A 2^12 as FP16;
+//   B     = b A + c A^2 in every CTA;
+//   X     <- a X + B X: TMEM times a while the partial sums are formed, then the
+//         product accumulates onto it.
+// The chunk of 64 columns of X in shared memory is at the same time a K-major
+// operand of X X^T and an MN-major one of B X.  A tall matrix is read and written
+// transposed.  One CTA to an SM: the launch asks for all shared memory, since CTAs
+// of two clusters that waited for each other's TMEM on two SMs would never finish.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "mx_gemm16.cuh"
+#include "mx_launch.h"
+
+namespace mxk {
+
+constexpr int kNsMaxSteps = 16;
+constexpr int kNsThreads = 256;  // two warps per TMEM lane quarter
+constexpr int kNsSmem = 232448;
+constexpr int kNsLogSA = 12;     // A and B are held times 2^12
+constexpr int kNsMaxCluster = 16;
+constexpr int kNsTurn = 65;      // floats between the rows of a turning tile of 32 x 64
+
+struct NsSmallArgs {
+  const void* g;
+  __nv_bfloat16* out;
+  int32_t* status;
+  uint64_t wait_ns;
+  int m, n;         // of one matrix
+  int slice;        // columns of the long side per CTA, a multiple of 64
+  int steps;
+  int log_sx;
+  float eps;
+  float coeffs[3 * kNsMaxSteps];
+};
+
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void st_cluster_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_b16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared::cluster.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// Byte offset of element (row, k) of a K-major operand of `rows` rows: chunks of
+// 64 k, each row 128 bytes, 16-byte pieces swizzled by the row.
+__device__ __forceinline__ uint32_t kmajor_at(int rows, int row, int k) {
+  return static_cast<uint32_t>((k >> 6) * rows * 128 + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) + (k & 7) * 2);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_constant__ NsSmallArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wgroup = warp >> 2;                   // which half of the columns
+  const int row = (warp & 3) * 32 + lane;         // TMEM lane and matrix row
+  const int rank = static_cast<int>(cluster_ctarank());
+  uint32_t cs_u;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs_u));
+  const int cs = static_cast<int>(cs_u);
+  const int batch = static_cast<int>(blockIdx.x) / cs;
+
+  const bool tall = args.m > args.n;
+  const int r = tall ? args.n : args.m, c = tall ? args.m : args.n;
+  const int rp = (r + 15) / 16 * 16;
+  const int slice = args.slice, chunks = slice / 64;
+  const int c0 = rank * slice;                    // the slice's first column; those at or beyond c are zeros
+  const int w = rp / cs > 0 ? (rp + cs - 1) / cs : 1;  // columns of A this CTA adds up (cs <= 16 divides rp)
+  const uint32_t misc = sbase;                                       // see below
+  const uint32_t xs = sbase + 1024;                                  // X, FP16
+  const uint32_t as = xs + chunks * rp * 128;                        // A
+  const uint32_t bs = as + (rp + 63) / 64 * rp * 128;                // B
+  const uint32_t recv = bs + (rp + 63) / 64 * rp * 128;              // [source][column][row] partial sums
+  const uint32_t turn = recv + warp * (32 * kNsTurn * 4);            // this warp's tile for turning rows into lanes
+  // misc: barrier 8, TMEM address 4, pad 4, block sums 8 x 8, cluster sums 16 x 8
+  const uint32_t bar = misc;
+  auto at = [&](uint32_t addr) { return smem + (addr - sbase); };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(at(misc + 8));
+  double* block_sums = reinterpret_cast<double*>(at(misc + 16));
+  const uint32_t cluster_sums = misc + 80;
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait_prior();
+  if (warp == 0) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync();  // every CTA of the cluster runs before its shared memory is written
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const uint32_t t_a = slice;                     // TMEM column of A's partial sum and of A^2
+  uint32_t parity = 0;
+  bool ok = true;
+  auto wait_mma = [&]() {
+    if (!wait16<false>(bar, parity, nullptr, args.wait_ns)) ok = false;
+    parity ^= 1u;
+    tc_fence_after();
+  };
+
+  // ---- read: raw values to TMEM, their squares summed in 64 bits over the cluster
+  const T* g = static_cast<const T*>(args.g) + static_cast<int64_t>(batch) * args.m * args.n;
+  double s = 0.0;
+  float* tile = reinterpret_cast<float*>(at(turn));
+  for (int j = wgroup; j < chunks; j += 2) {
+    const int col = c0 + j * 64;
+    if (!tall) {  // 64 columns of each of the warp's rows, lane by lane, then turned
+      const int row_w = row - lane;
+      float v[64];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const T* p = g + static_cast<int64_t>(row_w + i) * c + col + lane;
+        v[2 * i] = row_w + i < r && col + lane < c ? static_cast<float>(p[0]) : 0.0f;
+        v[2 * i + 1] = row_w + i < r && col + lane + 32 < c ? static_cast<float>(p[32]) : 0.0f;
+      }
+      __syncwarp();  // the tile has been read
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        tile[i * kNsTurn + lane] = v[2 * i];
+        tile[i * kNsTurn + lane + 32] = v[2 * i + 1];
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t raw[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int k = h * 32 + i;
+        const float v = !tall                        ? tile[lane * kNsTurn + k]
+                        : row < r && col + k < c ? static_cast<float>(g[static_cast<int64_t>(col + k) * r + row])
+                                                     : 0.0f;
+        s = fma(static_cast<double>(v), static_cast<double>(v), s);
+        raw[i] = __float_as_uint(v);
+      }
+      tc_st_32x32b_x32(t_row + j * 64 + h * 32, raw);
+    }
+  }
+  tc_wait_st();
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) block_sums[warp] = s;
+  __syncthreads();
+  if (tid < cs) {
+    double t = 0.0;
+    for (int i = 0; i < kNsThreads / 32; ++i) t += block_sums[i];
+    st_cluster_f64(map_to_rank(cluster_sums, tid) + rank * 8, t);
+  }
+  cluster_sync();
+  double sum = 0.0;
+  for (int i = 0; i < cs; ++i) sum += reinterpret_cast<const double*>(at(cluster_sums))[i];
+  const double f = sqrt(sum) + static_cast<double>(args.eps);
+  const bool usual = f > 0.0 && isfinite(f);  // else: zeros stay zeros, anything else becomes NaN
+  const int e = usual ? ilogb(f) : 0;
+  const float rest = usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("");
+  const float sa = static_cast<float>(1 << kNsLogSA), inv_sa = 1.0f / sa;
+
+  // FP16 copy of 32 columns of X for the products (rows of zeros up to rp)
+  auto put_x = [&](int col, const uint32_t (&v)[32]) {  // v: X 2^(sx + 12)
+    if (row >= rp) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = pack16(__uint_as_float(v[q * 8 + 2 * i]) * inv_sa, __uint_as_float(v[q * 8 + 2 * i + 1]) * inv_sa, 1);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(xs + kmajor_at(rp, row, col + q * 8)), "r"(o[0]),
+                   "r"(o[1]), "r"(o[2]), "r"(o[3])
+                   : "memory");
+    }
+  };
+  for (int j = wgroup; j < chunks; j += 2) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[32];
+      tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = __float_as_uint(scalbnf(__uint_as_float(v[i]), args.log_sx - e) * rest * sa);
+      tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
+      put_x(j * 64 + h * 32, v);
+    }
+  }
+  tc_wait_st();
+  const float a_scale = sa / scalbnf(1.0f, 2 * args.log_sx);
+
+  const uint32_t idesc_r = idesc_f16(128, rp, 1, 0, 0);
+#pragma unroll 1
+  for (int step = 0; step < args.steps; ++step) {
+    const float ca = args.coeffs[3 * step], cb = args.coeffs[3 * step + 1], cc = args.coeffs[3 * step + 2];
+    // ---- this slice's part of X X^T.  The 128 rows of the first operand reach
+    // past X's rp rows into what lies behind: accumulator rows that nobody reads.
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && elect_one()) {
+      tc_fence_after();
+      for (int k = 0; k < slice / 16; ++k) {
+        const uint64_t d = desc_kmajor_sw128(xs + (k >> 2) * rp * 128 + (k & 3) * 32);
+        tc_mma_f16(tmem + t_a, d, d, idesc_r, k != 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    __syncwarp();
+    // ---- meanwhile a X in TMEM.  The last two steps take (a I + B) X of the FP16 X
+    // instead, as the general form does: nothing multiplies X's rounding any more,
+    // and a X of one X with B X of another would only add the difference.
+    const bool add_x = step == 0 || step + 2 < args.steps;
+    for (int j = add_x ? wgroup : chunks; j < chunks; j += 2) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[32];
+        tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(ca * __uint_as_float(v[i]));
+        tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
+      }
+    }
+    tc_wait_st();
+    wait_mma();
+    // ---- partial sums to the CTAs that add them
+    for (int b = wgroup; b < rp / 16; b += 2) {
+      uint32_t v[16];
+      tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
+      tc_wait_ld();
+      if (row < rp) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int col = b * 16 + i, owner = col / w;
+          st_cluster_b32(map_to_rank(recv, owner) + static_cast<uint32_t>(((rank * w + col - owner * w) * 128 + row) * 4), v[i]);
+        }
+      }
+    }
+    cluster_sync();
+    // ---- added in rank order, and A 2^12 as FP16 to everyone.  Entry (row, col) is
+    // stored as (col, row): the rows of a warp are then consecutive.
+    if (row < rp) {
+      for (int q = wgroup; q < w; q += 2) {
+        const float* p = reinterpret_cast<const float*>(at(recv)) + q * 128 + row;
+        float t = 0.0f;
+        for (int i = 0; i < cs; ++i) t += p[i * w * 128];
+        const uint16_t v = static_cast<uint16_t>(pack16(t * a_scale, 0.0f, 1) & 0xFFFFu);
+        const uint32_t to = as + kmajor_at(rp, rank * w + q, row);
+        for (int i = 0; i < cs; ++i) st_cluster_b16(map_to_rank(to, i), v);
+      }
+    }
+    fence_proxy_async_all();
+    cluster_sync();
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    // ---- A^2
+    if (warp == 0 && elect_one()) {
+      tc_fence_after();
+      for (int k = 0; k < rp / 16; ++k) {
+        const uint64_t d = desc_kmajor_sw128(as + (k >> 2) * rp * 128 + (k & 3) * 32);
+        tc_mma_f16(tmem + t_a, d, d, idesc_r, k != 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    __syncwarp();
+    wait_mma();
+    // ---- B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)^2 (+ a 2^12 I)
+    for (int b = wgroup; b < rp / 16; b += 2) {
+      uint32_t v[16];
+      tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
+      tc_wait_ld();
+      if (row < rp) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t where = kmajor_at(rp, row, b * 16 + q * 8);
+          const uint4 a4 = *reinterpret_cast<const uint4*>(at(as + where));
+          const uint32_t u[4] = {a4.x, a4.y, a4.z, a4.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 af = unpack16(u[i], 1);
+            const int col = b * 16 + q * 8 + 2 * i;
+            const float d0 = !add_x && col == row ? ca * sa : 0.0f, d1 = !add_x && col + 1 == row ? ca * sa : 0.0f;
+            o[i] = pack16(fmaf(cb, af.x, fmaf(__uint_as_float(v[q * 8 + 2 * i]), cc * inv_sa, d0)),
+                          fmaf(cb, af.y, fmaf(__uint_as_float(v[q * 8 + 2 * i + 1]), cc * inv_sa, d1)), 1);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(bs + where), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    // ---- a X + B X, up to 256 columns an instruction
+    if (warp == 0 && elect_one()) {
+      tc_fence_after();
+      for (int n0 = 0; n0 < slice; n0 += 256) {
+        const uint32_t idesc = idesc_f16(128, slice - n0 < 256 ? slice - n0 : 256, 1, 0, 1);
+        for (int k = 0; k < rp / 16; ++k)
+          tc_mma_f16(tmem + n0, desc_kmajor_sw128(bs + (k >> 2) * rp * 128 + (k & 3) * 32),
+                     desc_mnmajor_sw128(xs + (n0 / 64) * rp * 128 + k * 2048, rp * 128), idesc, add_x || k != 0 ? 1u : 0u);
+      }
+      tc_commit(bar);
+    }
+    __syncwarp();
+    wait_mma();
+    if (step + 1 < args.steps) {
+      for (int j = wgroup; j < chunks; j += 2) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+          tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
+          tc_wait_ld();
+          put_x(j * 64 + h * 32, v);
+        }
+      }
+    }
+  }
+
+  // ---- out
+  const float last = inv_sa * scalbnf(1.0f, -args.log_sx);
+  __nv_bfloat16* out = args.out + static_cast<int64_t>(batch) * args.m * args.n;
+  for (int j = wgroup; j < chunks; j += 2) {
+    const int col = c0 + j * 64;
+    if (!tall) __syncwarp();  // the tile has been read
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[32];
+      tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int k = h * 32 + i;
+        const float x = __uint_as_float(v[i]) * last;
+        if (!tall)
+          tile[lane * kNsTurn + k] = x;
+        else if (row < r && col + k < c)
+          out[static_cast<int64_t>(col + k) * r + row] = __float2bfloat16_rn(x);
+      }
+    }
+    if (!tall) {
+      __syncwarp();
+      const int row_w = row - lane;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        __nv_bfloat16* p = out + static_cast<int64_t>(row_w + i) * c + col + lane;
+        if (row_w + i < r && col + lane < c) p[0] = __float2bfloat16_rn(tile[i * kNsTurn + lane]);
+        if (row_w + i < r && col + lane + 32 < c) p[32] = __float2bfloat16_rn(tile[i * kNsTurn + lane + 32]);
+      }
+    }
+  }
+  if (!ok && lane == 0) report(args.status, 0x4);
+  // no CTA leaves while another may still write into its shared memory
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ======================================================================= host
+
+constexpr int kNsDevices = 64;
+
+// Clusters of `cs` CTAs that the GPU holds at once (0: none).
+template <typename T>
+static int ns_clusters(int cs) {
+  static std::atomic<int> known[kNsDevices][kNsMaxCluster + 1];  // 0 unknown, else the number + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kNsDevices) return 0;
+  int v = known[dev][cs].load(std::memory_order_acquire);
+  if (v == 0) {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
+    cfg.blockDim = dim3(kNsThreads, 1, 1);
+    cfg.dynamicSmemBytes = kNsSmem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, ns_cluster_kernel<T>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    v = n + 1;
+    known[dev][cs].store(v, std::memory_order_release);
+  }
+  return v - 1;
+}
+
+static int ns_slice(int64_t c, int cs) { return static_cast<int>(((c + cs - 1) / cs + 63) / 64 * 64); }
+
+// Does a slice's X, A and partial sums fit TMEM's 512 columns, and everything shared memory?
+static bool ns_fits(int r, int slice, int cs) {
+  const int rp = (r + 15) / 16 * 16;
+  if (slice + rp > 512) return false;
+  const int operands = 1024 + slice / 64 * rp * 128 + 2 * ((rp + 63) / 64) * rp * 128;
+  const int partial = rp * 512, turn = kNsThreads / 32 * 32 * kNsTurn * 4;
+  // (behind B, the products' 128-row operands read (128 - rp) rows more: less than the turning tiles)
+  return 1024 + operands + (partial > turn ? partial : turn) <= kNsSmem;
+}
+
+template <typename T>
+static cudaError_t ns_small(const OrthoProblem& q, bool* taken, int num_sms, cudaStream_t stream) {
+  *taken = false;
+  const int64_t r = q.m < q.n ? q.m : q.n, c = q.m < q.n ? q.n : q.m;
+  if (r > 128 || c > kNsMaxCluster * 448) return cudaSuccess;
+  // the smallest cluster that holds the matrix; larger ones, down to 128 columns a
+  // CTA, while the whole batch fits the GPU at once
+  int cs = 0;
+  for (int s = 1; s <= kNsMaxCluster; s *= 2) {
+    if (!ns_fits(static_cast<int>(r), ns_slice(c, s), s)) continue;
+    const int held = ns_clusters<T>(s);
+    if (held == 0) break;
+    if (cs != 0 && (q.batch > held || ns_slice(c, s / 2) <= 128)) break;
+    cs = s;
+  }
+  if (cs == 0) return cudaSuccess;
+  *taken = true;
+  NsSmallArgs a = {};
+  a.g = q.g;
+  a.out = static_cast<__nv_bfloat16*>(q.out);
+  a.status = q.status;
+  a.wait_ns = wait_limit_ns();
+  a.m = static_cast<int>(q.m);
+  a.n = static_cast<int>(q.n);
+  a.slice = ns_slice(c, cs);
+  a.steps = q.steps;
+  a.log_sx = static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(c))));
+  a.eps = q.eps;
+  for (int i = 0; i < 3 * q.steps; ++i) a.coeffs[i] = q.coeffs[i];
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(static_cast<unsigned>(q.batch * cs), 1, 1);
+  cfg.blockDim = dim3(kNsThreads, 1, 1);
+  cfg.dynamicSmemBytes = kNsSmem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, ns_cluster_kernel<T>, a);
+}
+
+cudaError_t launch_orthogonalize_small(const OrthoProblem& q, bool* taken, int num_sms, cudaStream_t stream) {
+  return q.fp32 ? ns_small<float>(q, taken, num_sms, stream) : ns_small<__nv_bfloat16>(q, taken, num_sms, stream);
+}
+
+}  // namespace mxk

@@ -102,8 +102,40 @@ def test_shapes(mx, shape, dtype):
     check(g, out, [COEFFS] * 5, what=str(shape))
 
 
+EDGES = [(1, 16, 64), (1, 17, 65), (1, 2, 128), (2, 64, 129), (1, 65, 385), (1, 128, 768), (1, 127, 1025), (1, 64, 7168),
+         (1, 128, 6144), (1, 128, 6145), (1, 33, 7169), (20, 40, 700), (3, 1000, 128), (1, 3000, 100), (40, 128, 96)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", EDGES, ids=lambda s: "x".join(map(str, s)))
+def test_one_launch_form(mx, shape, dtype, monkeypatch):
+    """Around the sizes where the matrix just fits a cluster, both orientations,
+    more matrices than clusters; the general form gives the same within both errors."""
+    g = momentum(*shape, dtype, seed=21)
+    out, intact = guarded(shape, BF16)
+    mx.mx_orthogonalize(g, out=out)
+    torch.cuda.synchronize()
+    assert intact()
+    check(g, out, [COEFFS] * 5, what=str(shape))
+    monkeypatch.setenv("MX_ORTHO_CONFIG", "general")
+    check(g, mx.mx_orthogonalize(g), [COEFFS] * 5, what=f"{shape} general")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_shapes_general_form(mx, shape, dtype, monkeypatch):
+    monkeypatch.setenv("MX_ORTHO_CONFIG", "general")
+    g = momentum(*shape, dtype, seed=1)
+    out, intact = guarded(shape, BF16)
+    mx.mx_orthogonalize(g, out=out)
+    torch.cuda.synchronize()
+    assert intact()
+    check(g, out, [COEFFS] * 5, what=str(shape))
+
+
 @pytest.mark.parametrize("cfg", ["0", "1", "4"])
 def test_every_kernel(mx, cfg, monkeypatch):
+    monkeypatch.setenv("MX_ORTHO_CONFIG", "general")
     monkeypatch.setenv("MX_GEMM16_CONFIG", cfg)
     for shape in ((2, 300, 520), (1, 520, 296), (2, 71, 77), (1, 640, 641)):
         for dtype in (BF16, FP32):
@@ -143,10 +175,12 @@ def test_two_dimensions_in_place_and_workspace(mx):
     assert torch.equal(mx.mx_orthogonalize(g, out=g), want)
 
 
-@pytest.mark.parametrize("shape", [(64, 136), (136, 64), (60, 77)], ids=str)
-def test_special_matrices(mx, shape):
+@pytest.mark.parametrize("form", ["", "general"])
+@pytest.mark.parametrize("shape", [(64, 136), (136, 64), (60, 77), (136, 140)], ids=str)
+def test_special_matrices(mx, shape, form, monkeypatch):
     """Zeros give zeros; a NaN or an infinity spoils its own matrix only; norms at
     the ends of the types' ranges."""
+    monkeypatch.setenv("MX_ORTHO_CONFIG", form)
     g = momentum(6, *shape, FP32, seed=7, scale=1.0)
     g[1] = 0.0
     g[2, 3, 5] = float("nan")
