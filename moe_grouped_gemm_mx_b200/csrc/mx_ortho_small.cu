@@ -32,11 +32,12 @@
 namespace mxk {
 
 constexpr int kNsMaxSteps = 16;
-constexpr int kNsThreads = 256;  // two warps per TMEM lane quarter
+constexpr int kNsThreads = 512;  // four warps per TMEM lane quarter
+constexpr int kNsGroups = kNsThreads / 128;
 constexpr int kNsSmem = 232448;
 constexpr int kNsLogSA = 12;     // A and B are held times 2^12
 constexpr int kNsMaxCluster = 16;
-constexpr int kNsTurn = 65;      // floats between the rows of a turning tile of 32 x 64
+constexpr int kNsTurn = 65;      // 32-bit words between the rows of a turning tile of 16 x 64
 
 struct NsSmallArgs {
   const void* g;
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wgroup = warp >> 2;                   // which half of the columns
+  const int wgroup = warp >> 2;                   // which chunks of 64 columns
   const int row = (warp & 3) * 32 + lane;         // TMEM lane and matrix row
   const int rank = static_cast<int>(cluster_ctarank());
   uint32_t cs_u;
@@ -101,6 +102,8 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const int r = tall ? args.n : args.m, c = tall ? args.m : args.n;
   const int rp = (r + 15) / 16 * 16;
   const int slice = args.slice, chunks = slice / 64;
+  // a warp whose 32 rows lie behind the matrix has no chunks
+  const int first = (warp & 3) * 32 < rp ? wgroup : chunks, first16 = (warp & 3) * 32 < rp ? wgroup : rp / 16;
   const int c0 = rank * slice;                    // the slice's first column; those at or beyond c are zeros
   const int w = rp / cs > 0 ? (rp + cs - 1) / cs : 1;  // columns of A this CTA adds up (cs <= 16 divides rp)
   const uint32_t misc = sbase;                                       // see below
@@ -108,13 +111,13 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const uint32_t as = xs + chunks * rp * 128;                        // A
   const uint32_t bs = as + (rp + 63) / 64 * rp * 128;                // B
   const uint32_t recv = bs + (rp + 63) / 64 * rp * 128;              // [source][column][row] partial sums
-  const uint32_t turn = recv + warp * (32 * kNsTurn * 4);            // this warp's tile for turning rows into lanes
-  // misc: barrier 8, TMEM address 4, pad 4, block sums 8 x 8, cluster sums 16 x 8
+  const uint32_t turn = recv + warp * (16 * kNsTurn * 4);            // this warp's tile for turning rows into lanes
+  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8
   const uint32_t bar = misc;
   auto at = [&](uint32_t addr) { return smem + (addr - sbase); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(at(misc + 8));
   double* block_sums = reinterpret_cast<double*>(at(misc + 16));
-  const uint32_t cluster_sums = misc + 80;
+  const uint32_t cluster_sums = misc + 144;
 
   if (tid == 0) {
     mbar_init(bar, 1);
@@ -142,45 +145,98 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
 
   // ---- read: raw values to TMEM, their squares summed in 64 bits over the cluster
   const T* g = static_cast<const T*>(args.g) + static_cast<int64_t>(batch) * args.m * args.n;
-  double s = 0.0;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
   float* tile = reinterpret_cast<float*>(at(turn));
-  for (int j = wgroup; j < chunks; j += 2) {
-    const int col = c0 + j * 64;
-    if (!tall) {  // 64 columns of each of the warp's rows, lane by lane, then turned
-      const int row_w = row - lane;
-      float v[64];
+  constexpr int V = 16 / static_cast<int>(sizeof(T));  // values of a 16-byte load
+  const bool wide_loads = !tall && c % V == 0;
+  for (int j = first; j < chunks; j += kNsGroups) {
+    const int col = c0 + j * 64, row_w = row - lane;
+    uint32_t raw[64];
+    if (!tall) {
+      // rows as they lie, 16 of the warp's at a time through the turning tile
+      constexpr int LANES = 64 / V, ROWS = 32 / LANES;  // lanes of a row, rows of a load
+      uint4 q[32 / ROWS];
+      uint32_t u16[sizeof(T) == 2 ? 32 : 1];  // unaligned BF16 rows: columns lane and lane + 32
+      if (!wide_loads && sizeof(T) == 2) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(g) + static_cast<int64_t>(row_w) * c + col + lane;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const T* p = g + static_cast<int64_t>(row_w + i) * c + col + lane;
-        v[2 * i] = row_w + i < r && col + lane < c ? static_cast<float>(p[0]) : 0.0f;
-        v[2 * i + 1] = row_w + i < r && col + lane + 32 < c ? static_cast<float>(p[32]) : 0.0f;
+        for (int i = 0; i < (sizeof(T) == 2 ? 32 : 0); ++i, p += c) {
+          const uint32_t lo = row_w + i < r && col + lane < c ? __ldg(p) : 0u;
+          const uint32_t hi = row_w + i < r && col + lane + 32 < c ? __ldg(p + 32) : 0u;
+          u16[i] = lo | hi << 16;
+        }
       }
-      __syncwarp();  // the tile has been read
+      if (wide_loads) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        tile[i * kNsTurn + lane] = v[2 * i];
-        tile[i * kNsTurn + lane + 32] = v[2 * i + 1];
+        for (int i = 0; i < 32 / ROWS; ++i) {
+          const int y = row_w + i * ROWS + lane / LANES, x = col + lane % LANES * V;
+          q[i] = y < r && x < c ? __ldg(reinterpret_cast<const uint4*>(g + static_cast<int64_t>(y) * c + x)) : make_uint4(0, 0, 0, 0);
+        }
       }
-      __syncwarp();
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        __syncwarp();  // the tile has been read
+        if (wide_loads) {
+#pragma unroll
+          for (int i = 0; i < 16 / ROWS; ++i) {
+            const uint4 w4 = q[part * (16 / ROWS) + i];
+            const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
+            float* to = tile + (i * ROWS + lane / LANES) * kNsTurn + lane % LANES * V;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              if constexpr (sizeof(T) == 4) {
+                to[p] = __uint_as_float(u[p]);
+              } else {
+                const float2 f2 = unpack16(u[p], 0);
+                to[2 * p] = f2.x;
+                to[2 * p + 1] = f2.y;
+              }
+            }
+          }
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 f2 = unpack16(u16[part * 16 + i], 0);
+            tile[i * kNsTurn + lane] = f2.x;
+            tile[i * kNsTurn + lane + 32] = f2.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int y = row_w + part * 16 + i;
+            const T* p = g + static_cast<int64_t>(y) * c + col + lane;
+            tile[i * kNsTurn + lane] = y < r && col + lane < c ? static_cast<float>(p[0]) : 0.0f;
+            tile[i * kNsTurn + lane + 32] = y < r && col + lane + 32 < c ? static_cast<float>(p[32]) : 0.0f;
+          }
+        }
+        __syncwarp();
+        if (lane / 16 == part) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(tile[(lane & 15) * kNsTurn + k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 64; ++k)
+        raw[k] = row < r && col + k < c
+                     ? __float_as_uint(static_cast<float>(g[static_cast<int64_t>(col + k) * r + row])) : 0u;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t raw[32];
+      uint32_t v[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const int k = h * 32 + i;
-        const float v = !tall                        ? tile[lane * kNsTurn + k]
-                        : row < r && col + k < c ? static_cast<float>(g[static_cast<int64_t>(col + k) * r + row])
-                                                     : 0.0f;
-        s = fma(static_cast<double>(v), static_cast<double>(v), s);
-        raw[i] = __float_as_uint(v);
+        v[i] = raw[h * 32 + i];
+        const double x = __uint_as_float(v[i]);
+        s[i & 3] = fma(x, x, s[i & 3]);
       }
-      tc_st_32x32b_x32(t_row + j * 64 + h * 32, raw);
+      tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
     }
   }
   tc_wait_st();
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xFFFFFFFFu, s, o);
-  if (lane == 0) block_sums[warp] = s;
+  double own = (s[0] + s[1]) + (s[2] + s[3]);
+  for (int o = 16; o > 0; o >>= 1) own += __shfl_down_sync(0xFFFFFFFFu, own, o);
+  if (lane == 0) block_sums[warp] = own;
   __syncthreads();
   if (tid < cs) {
     double t = 0.0;
@@ -195,6 +251,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const int e = usual ? ilogb(f) : 0;
   const float rest = usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("");
   const float sa = static_cast<float>(1 << kNsLogSA), inv_sa = 1.0f / sa;
+  // 2^(sx - e) in two halves: neither leaves FP32's range
+  const int shift = args.log_sx - e;
+  const float up0 = scalbnf(1.0f, shift / 2), up1 = scalbnf(1.0f, shift - shift / 2) , up2 = rest * sa;
 
   // FP16 copy of 32 columns of X for the products (rows of zeros up to rp)
   auto put_x = [&](int col, const uint32_t (&v)[32]) {  // v: X 2^(sx + 12)
@@ -210,7 +269,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
                    : "memory");
     }
   };
-  for (int j = wgroup; j < chunks; j += 2) {
+  for (int j = first; j < chunks; j += kNsGroups) {
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       uint32_t v[32];
@@ -218,7 +277,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
       tc_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        v[i] = __float_as_uint(scalbnf(__uint_as_float(v[i]), args.log_sx - e) * rest * sa);
+        v[i] = __float_as_uint(__uint_as_float(v[i]) * up0 * up1 * up2);
       tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
       put_x(j * 64 + h * 32, v);
     }
@@ -248,7 +307,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // instead, as the general form does: nothing multiplies X's rounding any more,
     // and a X of one X with B X of another would only add the difference.
     const bool add_x = step == 0 || step + 2 < args.steps;
-    for (int j = add_x ? wgroup : chunks; j < chunks; j += 2) {
+    for (int j = add_x ? first : chunks; j < chunks; j += kNsGroups) {
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t v[32];
@@ -262,7 +321,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     tc_wait_st();
     wait_mma();
     // ---- partial sums to the CTAs that add them
-    for (int b = wgroup; b < rp / 16; b += 2) {
+    for (int b = first16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
       tc_wait_ld();
@@ -278,7 +337,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // ---- added in rank order, and A 2^12 as FP16 to everyone.  Entry (row, col) is
     // stored as (col, row): the rows of a warp are then consecutive.
     if (row < rp) {
-      for (int q = wgroup; q < w; q += 2) {
+      for (int q = wgroup; q < w; q += kNsGroups) {
         const float* p = reinterpret_cast<const float*>(at(recv)) + q * 128 + row;
         float t = 0.0f;
         for (int i = 0; i < cs; ++i) t += p[i * w * 128];
@@ -304,7 +363,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     __syncwarp();
     wait_mma();
     // ---- B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)^2 (+ a 2^12 I)
-    for (int b = wgroup; b < rp / 16; b += 2) {
+    for (int b = first16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
       tc_wait_ld();
@@ -345,7 +404,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     __syncwarp();
     wait_mma();
     if (step + 1 < args.steps) {
-      for (int j = wgroup; j < chunks; j += 2) {
+      for (int j = first; j < chunks; j += kNsGroups) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t v[32];
@@ -360,32 +419,50 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   // ---- out
   const float last = inv_sa * scalbnf(1.0f, -args.log_sx);
   __nv_bfloat16* out = args.out + static_cast<int64_t>(batch) * args.m * args.n;
-  for (int j = wgroup; j < chunks; j += 2) {
-    const int col = c0 + j * 64;
-    if (!tall) __syncwarp();  // the tile has been read
+  for (int j = first; j < chunks; j += kNsGroups) {
+    const int col = c0 + j * 64, row_w = row - lane;
+    uint32_t w2[32];  // pairs of columns
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t v[32];
       tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
       tc_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int k = h * 32 + i;
-        const float x = __uint_as_float(v[i]) * last;
-        if (!tall)
-          tile[lane * kNsTurn + k] = x;
-        else if (row < r && col + k < c)
-          out[static_cast<int64_t>(col + k) * r + row] = __float2bfloat16_rn(x);
-      }
+      for (int i = 0; i < 16; ++i)
+        w2[h * 16 + i] = pack16(__uint_as_float(v[2 * i]) * last, __uint_as_float(v[2 * i + 1]) * last, 0);
     }
-    if (!tall) {
-      __syncwarp();
-      const int row_w = row - lane;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        __nv_bfloat16* p = out + static_cast<int64_t>(row_w + i) * c + col + lane;
-        if (row_w + i < r && col + lane < c) p[0] = __float2bfloat16_rn(tile[i * kNsTurn + lane]);
-        if (row_w + i < r && col + lane + 32 < c) p[32] = __float2bfloat16_rn(tile[i * kNsTurn + lane + 32]);
+    if (tall) {
+#pragma unroll
+      for (int k = 0; k < 64; ++k)
+        if (row < r && col + k < c)
+          reinterpret_cast<uint16_t*>(out)[static_cast<int64_t>(col + k) * r + row] = static_cast<uint16_t>(w2[k / 2] >> (k & 1) * 16);
+    } else {
+      // 16 rows of 32 pairs at a time through the turning tile
+      uint32_t* pairs = reinterpret_cast<uint32_t*>(tile);
+      constexpr int STEP = kNsTurn / 2 + 1;  // 33
+      static_assert(16 * STEP <= 16 * kNsTurn, "the tile holds them");
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        __syncwarp();
+        if (lane / 16 == part) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) pairs[(lane & 15) * STEP + k] = w2[k];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int y = row_w + part * 16 + i, x = col + 2 * lane;
+          const uint32_t u = pairs[i * STEP + lane];
+          uint16_t* o = reinterpret_cast<uint16_t*>(out) + static_cast<int64_t>(y) * c + x;
+          if (y < r && x < c) {
+            if (c % 2 == 0) {
+              *reinterpret_cast<uint32_t*>(o) = u;
+            } else {
+              o[0] = static_cast<uint16_t>(u);
+              if (x + 1 < c) o[1] = static_cast<uint16_t>(u >> 16);
+            }
+          }
+        }
       }
     }
   }
@@ -442,7 +519,7 @@ static bool ns_fits(int r, int slice, int cs) {
   const int rp = (r + 15) / 16 * 16;
   if (slice + rp > 512) return false;
   const int operands = 1024 + slice / 64 * rp * 128 + 2 * ((rp + 63) / 64) * rp * 128;
-  const int partial = rp * 512, turn = kNsThreads / 32 * 32 * kNsTurn * 4;
+  const int partial = rp * 512, turn = kNsThreads / 32 * 16 * kNsTurn * 4;
   // (behind B, the products' 128-row operands read (128 - rp) rows more: less than the turning tiles)
   return 1024 + operands + (partial > turn ? partial : turn) <= kNsSmem;
 }
