@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             if (c == 64) release();
             continue;
           }
+          uint4 res[8], low[8];
+          if constexpr (EPI != kEpiPlain) g16_load_res<64>(args, args.res, tl.group, row, col0, args.n, valid, res);
+          if constexpr (EPI == kEpiPoly) g16_load_res<64>(args, args.res_lo, tl.group, row, col0, args.n, valid, low);
           float v[64];
           {
             uint32_t raw[2][32];
@@ -395,17 +398,29 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             for (int j = 0; j < 32; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
             put(map, w, col0, row_w, z_out);
           };
-          g16_epilogue<EPI, 64>(args, v, tl.group, row, col0, valid, scale);
           if constexpr (EPI == kEpiLinear) {
+            if (args.bias != nullptr) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                if (col0 + q * 8 < args.n) {
+                  float b[8];
+                  load8(static_cast<const uint16_t*>(args.bias) + col0 + q * 8, args.op_fp16, b);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[q * 8 + j] += b[j];
+                }
+              }
+            }
             if (args.z != nullptr) put64(&tmap_z);
-            g16_activate<64>(args, v, row, col0, valid);
+            g16_activate<64>(args, v, res);
+          } else {
+            g16_epilogue<EPI, 64>(args, v, res, low, nullptr, tl.group, row, col0, scale);
           }
           if (tma)
             put64(&tmap_d);
           else if (valid)
-            g16_store_row<64>(args, args.d, v, tl.group, row, col0);
+            g16_store_row<64>(args, args.d, v, tl.group, row, col0, args.n);
           if constexpr (EPI == kEpiPoly) {
-            if (args.sym && tl.mb != tl.nb && valid) g16_store_mirror<64>(args, v, tl.group, row, col0);
+            if (args.sym && tl.mb != tl.nb && valid) g16_store_mirror<64>(args, v, tl.group, row, col0, args.n);
             if (args.z != nullptr) {
               g16_remainder<64>(args, v);
               put64(&tmap_z);
@@ -447,7 +462,8 @@ struct S16Layout {
   static constexpr int NUM_BARS = 2 * STAGES + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = (OFF_MISC + 16 + 15) / 16 * 16;
-  static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
+  static constexpr int OFF_BIAS = (OFF_TAB + (kMaxGroups / kTabStep + 1) * 4 + 15) / 16 * 16;
+  static constexpr int BYTES = OFF_BIAS + 128 * 4;
   static constexpr int ALLOC = BYTES + 1024;
   // partial sums of the other CTAs (at most 7 slices of 16 columns x 128 rows,
   // or 1 of 64) take the operand ring's place once the MMAs are done
@@ -474,6 +490,7 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   volatile uint32_t* tmem_slot = misc + 0;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   int32_t* tab = reinterpret_cast<int32_t*>(smem + L::OFF_TAB);
+  float* bias = reinterpret_cast<float*>(smem + L::OFF_BIAS);
   auto full_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * s; };
   auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
   const uint32_t acc_bar = sbase + L::OFF_BAR + 8u * (2 * S);
@@ -604,7 +621,27 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
   const int row = tl.row0 + r;
   const bool valid = row < tl.rows_end;
+  const int width = kS16T / splits;  // columns of the tile this CTA finishes
+  const int col_p = tl.nb * kS16T + part * width;
+  const int col_end = col_p + width < args.n ? col_p + width : args.n;
+  // what the epilogue reads comes while the operands do: C and the residual into
+  // registers, the bias as FP32 into shared memory
+  uint4 res[4][4], low[4][4];
   if (warp >= 2) {
+    if constexpr (EPI == kEpiLinear) {
+      if (args.bias != nullptr && col_p + r < col_end) {
+        const uint16_t b = __ldg(static_cast<const uint16_t*>(args.bias) + col_p + r);
+        bias[r] = unpack16(b, args.op_fp16).x;
+      }
+      named_barrier_sync(1, 128);
+    }
+    if constexpr (EPI != kEpiPlain) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        g16_load_res<32>(args, args.res, tl.group, row, col_p + c * 32, col_end, valid, res[c]);
+        if constexpr (EPI == kEpiPoly) g16_load_res<32>(args, args.res_lo, tl.group, row, col_p + c * 32, col_end, valid, low[c]);
+      }
+    }
     got = wait16<false>(acc_bar, 0, abort_flag, args.wait_ns);
     got = __all_sync(0xFFFFFFFFu, got);
     if (!got && lane == 0) {
@@ -613,7 +650,21 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
     }
     tc_fence_after();
   }
-  const int width = kS16T / splits;  // columns of the tile this CTA finishes
+  // 32 columns of this thread's accumulator row (16 where a CTA has no more)
+  auto columns = [&](int col_t, uint32_t (&raw)[32]) {
+    if (width >= 32) {
+      tc_ld_32x32b_x32(t_row + col_t, raw);
+    } else {
+      uint32_t r16[16];
+      tc_ld_32x32b_x16(t_row + col_t, r16);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        raw[j] = r16[j];
+        raw[16 + j] = 0;
+      }
+    }
+    tc_wait_ld();
+  };
   if (splits > 1) {
     // every CTA's MMAs have read their operands: the rings can take partial sums
     cluster_sync();
@@ -624,13 +675,13 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
         // [slot][quad of columns][row] of float4: a warp's 32 rows are 512 bytes
         const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>((slot * (width / 4) * kS16T + r) * 16);
 #pragma unroll 1
-        for (int c = 0; c < width; c += 16) {
-          uint32_t raw[16];
-          tc_ld_32x32b_x16(t_row + owner * width + c, raw);
-          tc_wait_ld();
+        for (int c = 0; c < width; c += 32) {
+          uint32_t raw[32];
+          columns(owner * width + c, raw);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_cluster_v4(dst + (c / 4 + j) * kS16T * 16, raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            if (c + j * 4 < width)
+              st_cluster_v4(dst + (c / 4 + j) * kS16T * 16, raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
         }
       }
     }
@@ -638,40 +689,42 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   }
   if (warp >= 2 && got && tl.row0 + quarter * 32 < tl.rows_end) {
     const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
-#pragma unroll 1
-    for (int c = 0; c < width; c += 16) {
-      const int col_t = part * width + c;
-      const int col0 = tl.nb * kS16T + col_t;
-      if (col0 >= args.n) break;
-      uint32_t raw[16];
-      tc_ld_32x32b_x16(t_row + col_t, raw);
-      tc_wait_ld();
-      float v[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
-      for (int slot = 0; slot < splits - 1; ++slot) {
-        const float4* src = reinterpret_cast<const float4*>(smem) + ((slot * width + c) / 4) * kS16T + r;
+    for (int ci = 0; ci < 4; ++ci) {
+      const int c = ci * 32;
+      const int col0 = col_p + c;
+      if (c < width && col0 < args.n) {
+        uint32_t raw[32];
+        columns(part * width + c, raw);
+        float v[32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 f = src[j * kS16T];
-          v[4 * j] += f.x;
-          v[4 * j + 1] += f.y;
-          v[4 * j + 2] += f.z;
-          v[4 * j + 3] += f.w;
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+        for (int slot = 0; slot < splits - 1; ++slot) {
+          const float4* src = reinterpret_cast<const float4*>(smem) + ((slot * width + c) / 4) * kS16T + r;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (c + j * 4 < width) {
+              const float4 f = src[j * kS16T];
+              v[4 * j] += f.x;
+              v[4 * j + 1] += f.y;
+              v[4 * j + 2] += f.z;
+              v[4 * j + 3] += f.w;
+            }
+          }
         }
-      }
-      g16_epilogue<EPI, 16>(args, v, tl.group, row, col0, valid, scale);
-      if constexpr (EPI == kEpiLinear) {
-        if (args.z != nullptr && valid) g16_store_row<16>(args, args.z, v, tl.group, row, col0);
-        g16_activate<16>(args, v, row, col0, valid);
-      }
-      if (valid) {
-        g16_store_row<16>(args, args.d, v, tl.group, row, col0);
-        if constexpr (EPI == kEpiPoly) {
-          if (args.sym && tl.mb != tl.nb) g16_store_mirror<16>(args, v, tl.group, row, col0);
-          if (args.z != nullptr) {
-            g16_remainder<16>(args, v);
-            g16_store_row<16>(args, args.z, v, tl.group, row, col0);
+        g16_epilogue<EPI, 32>(args, v, res[ci], low[ci], bias + c, tl.group, row, col0, scale);
+        if constexpr (EPI == kEpiLinear) {
+          if (args.z != nullptr && valid) g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
+          g16_activate<32>(args, v, res[ci]);
+        }
+        if (valid) {
+          g16_store_row<32>(args, args.d, v, tl.group, row, col0, col_end);
+          if constexpr (EPI == kEpiPoly) {
+            if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, col_end);
+            if (args.z != nullptr) {
+              g16_remainder<32>(args, v);
+              g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
+            }
           }
         }
       }

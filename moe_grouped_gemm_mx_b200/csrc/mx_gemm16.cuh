@@ -291,11 +291,13 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, int fp16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// v[0..8) += or = eight 16-bit values at p
-__device__ __forceinline__ void load8(const void* p, int fp16, float (&f)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void split8(const uint4 w, int fp16, float (&f)[8]) {
   const float2 a = unpack16(w.x, fp16), b = unpack16(w.y, fp16), c = unpack16(w.z, fp16), d = unpack16(w.w, fp16);
   f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
+}
+
+__device__ __forceinline__ void load8(const void* p, int fp16, float (&f)[8]) {
+  split8(__ldg(reinterpret_cast<const uint4*>(p)), fp16, f);
 }
 
 // ---------------------------------------------------------------- activations
@@ -348,46 +350,44 @@ __device__ __forceinline__ float g16_scale(const G16Args& a, int group) {
 }
 
 // The epilogue's arithmetic on C consecutive columns from col0 of one row, in
-// place.  `valid`: the row is the group's; columns at or beyond n hold values
-// that are never stored.
+// place.  `valid`: the row is the group's; columns at or beyond `end` (n, or where
+// another CTA's begin) hold values that are never stored.  C's and the residual's
+// values come with the call (g16_load_res, zeros where there is none).
 //
 // First part.  Linear: the pre-activation acc + bias.  Poly: D itself; scale is
 // g16_scale of the tile's group.
 template <int EPI, int C>
-__device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], int group, int64_t row, int col0, bool valid,
+__device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], const uint4 (&res)[C / 8],
+                                             const uint4 (&low)[C / 8], const float* bias, int group, int64_t row, int col0,
                                              float scale) {
   if constexpr (EPI == kEpiLinear) {
     if (a.bias != nullptr) {
 #pragma unroll
-      for (int g = 0; g < C / 8; ++g) {
-        if (col0 + g * 8 < a.n) {
-          float b[8];
-          load8(static_cast<const uint16_t*>(a.bias) + col0 + g * 8, a.op_fp16, b);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
-        }
+      for (int j = 0; j < C; j += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(bias + j);
+        v[j] += b.x;
+        v[j + 1] += b.y;
+        v[j + 2] += b.z;
+        v[j + 3] += b.w;
       }
     }
   } else if constexpr (EPI == kEpiPoly) {
 #pragma unroll
     for (int j = 0; j < C; ++j) v[j] *= scale;
-    if (a.res != nullptr && valid) {
-      const int64_t at = group * a.res_batch + row * a.res_ld + col0;
+    if (a.res != nullptr) {
       const float beta = a.scale != nullptr && a.scale_pow == 1 ? a.beta * __ldg(a.scale + group) : a.beta;
 #pragma unroll
       for (int g = 0; g < C / 8; ++g) {
-        if (col0 + g * 8 < a.n) {
-          float b[8];
-          load8(static_cast<const uint16_t*>(a.res) + at + g * 8, a.op_fp16, b);
-          if (a.res_lo != nullptr) {
-            float l[8];
-            load8(static_cast<const uint16_t*>(a.res_lo) + at + g * 8, a.op_fp16, l);
+        float b[8];
+        split8(res[g], a.op_fp16, b);
+        if (a.res_lo != nullptr) {
+          float l[8];
+          split8(low[g], a.op_fp16, l);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] += l[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[g * 8 + j] = fmaf(beta, b[j], v[g * 8 + j]);
+          for (int j = 0; j < 8; ++j) b[j] += l[j];
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[g * 8 + j] = fmaf(beta, b[j], v[g * 8 + j]);
       }
     }
     if (a.diag != 0.0f) {
@@ -403,7 +403,7 @@ __device__ __forceinline__ void g16_epilogue(const G16Args& a, float (&v)[C], in
 
 // Second part of the linear epilogue: activation and residual.
 template <int C>
-__device__ __forceinline__ void g16_activate(const G16Args& a, float (&v)[C], int64_t row, int col0, bool valid) {
+__device__ __forceinline__ void g16_activate(const G16Args& a, float (&v)[C], const uint4 (&res)[C / 8]) {
   switch (a.act) {  // one loop for each, not a choice for each value
     case 1:
 #pragma unroll
@@ -423,18 +423,26 @@ __device__ __forceinline__ void g16_activate(const G16Args& a, float (&v)[C], in
       break;
     default: break;
   }
-  if (a.res != nullptr && valid) {
-    const uint16_t* res = static_cast<const uint16_t*>(a.res) + row * a.res_ld + col0;
+  if (a.res != nullptr) {
 #pragma unroll
     for (int g = 0; g < C / 8; ++g) {
-      if (col0 + g * 8 < a.n) {
-        float b[8];
-        load8(res + g * 8, a.op_fp16, b);
+      float b[8];
+      split8(res[g], a.op_fp16, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
-      }
+      for (int j = 0; j < 8; ++j) v[g * 8 + j] += b[j];
     }
   }
+}
+
+// C columns from col0 of a row of the residual (or C, or its low half).
+template <int C>
+__device__ __forceinline__ void g16_load_res(const G16Args& a, const void* base, int group, int64_t row, int col0, int end,
+                                             bool valid, uint4 (&res)[C / 8]) {
+  const uint16_t* p = static_cast<const uint16_t*>(base) + group * a.res_batch + row * a.res_ld + col0;
+#pragma unroll
+  for (int g = 0; g < C / 8; ++g)
+    res[g] = base != nullptr && valid && col0 + g * 8 < end ? __ldg(reinterpret_cast<const uint4*>(p + g * 8))
+                                                            : make_uint4(0, 0, 0, 0);
 }
 
 // What rounding the values to the output type leaves.
@@ -449,15 +457,15 @@ __device__ __forceinline__ void g16_remainder(const G16Args& a, float (&v)[C]) {
   }
 }
 
-// C columns of one row to global memory, whole groups of 8 columns inside n
+// C columns of one row to global memory, whole groups of 8 columns before `end`
 // (rows are padded to a multiple of 8 elements).
 template <int C>
 __device__ __forceinline__ void g16_store_row(const G16Args& a, void* out, const float (&v)[C], int group, int64_t row,
-                                              int col0) {
+                                              int col0, int end) {
   const int64_t at = group * a.d_batch + row * a.d_ld + col0;
 #pragma unroll
   for (int g = 0; g < C / 8; ++g) {
-    if (col0 + g * 8 < a.n) {
+    if (col0 + g * 8 < end) {
       const float* p = v + g * 8;
       if (a.out_type == 2) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + g * 8);
@@ -476,13 +484,13 @@ __device__ __forceinline__ void g16_store_row(const G16Args& a, void* out, const
 // becomes row col0 + j; a warp's 32 rows are 64 consecutive bytes there.
 template <int C>
 __device__ __forceinline__ void g16_store_mirror(const G16Args& a, const float (&v)[C], int group, int64_t row,
-                                                 int col0) {
+                                                 int col0, int end) {
   uint16_t* out = static_cast<uint16_t*>(a.d) + group * a.d_batch + row;
 #pragma unroll
   for (int j = 0; j < C; j += 2) {
     const uint32_t w = pack16(v[j], v[j + 1], a.out_type == 1);
-    if (col0 + j < a.n) out[(col0 + j) * a.d_ld] = static_cast<uint16_t>(w & 0xFFFFu);
-    if (col0 + j + 1 < a.n) out[(col0 + j + 1) * a.d_ld] = static_cast<uint16_t>(w >> 16);
+    if (col0 + j < end) out[(col0 + j) * a.d_ld] = static_cast<uint16_t>(w & 0xFFFFu);
+    if (col0 + j + 1 < end) out[(col0 + j + 1) * a.d_ld] = static_cast<uint16_t>(w >> 16);
   }
 }
 
