@@ -10,6 +10,7 @@
 //      warp 0      TMA producer (both CTAs): 64 elements of K per stage
 //      warp 1      MMA issuer (leader), K = 16 per instruction
 //      warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
+//                  (linear: warps 2-17, four per quarter, 64 columns each)
 //      warp 10     ragged K only (both CTAs): clears the rows of the stage that
 //                  lie behind the group's last token before the MMAs read them
 //
@@ -31,22 +32,31 @@ namespace mxk {
 
 // ======================================================================= CTA-pair kernel
 
-constexpr int kP16Stages = 6;
-constexpr int kP16EpiWarps = 8;
-constexpr int kP16Threads = 32 * (2 + kP16EpiWarps + 1);
+// Epilogue warps: the linear epilogue's arithmetic (an activation is some 20
+// instructions a value) wants four to a scheduler; the others keep 8 with more
+// registers.  One more warp clears rows (ragged K; never with the linear epilogue).
+__host__ __device__ constexpr int p16_epi_warps(int epi) { return epi == kEpiLinear ? 16 : 8; }
+__host__ __device__ constexpr int p16_threads(int epi) { return 32 * (2 + p16_epi_warps(epi) + (epi == kEpiLinear ? 0 : 1)); }
 constexpr int kP16TM = 256, kP16TN = 256;
 constexpr int kP16K = 64;     // elements of K per stage
 constexpr int kP16Seg = 512;  // kEpiSum: K per partial sum
 
+// The linear epilogue's 16 warps take a stage's place for their staging tiles,
+// where the residual's rows wait for the sum (five stages cost about 1 % of a long
+// product).
+template <int EPI>
 struct P16Layout {
+  static constexpr int STAGES = EPI == kEpiLinear ? 5 : 6;
+  static constexpr int WARPS = p16_epi_warps(EPI);
   static constexpr int OP_BYTES = 128 * 128;        // 16 KB: one operand's half tile of a stage
   static constexpr int OFF_A = 0;
-  static constexpr int OFF_B = OFF_A + kP16Stages * OP_BYTES;
-  static constexpr int OFF_STG = OFF_B + kP16Stages * OP_BYTES;
-  static constexpr int STG_BYTES = 32 * 128;        // per epilogue warp: 32 rows of 128 bytes
-  static constexpr int OFF_BAR = OFF_STG + kP16EpiWarps * STG_BYTES;
-  // full, empty, tail landed, tail cleared per stage; accumulator full and empty (2 each); drain
-  static constexpr int NUM_BARS = 4 * kP16Stages + 5;
+  static constexpr int OFF_B = OFF_A + STAGES * OP_BYTES;
+  static constexpr int OFF_STG = OFF_B + STAGES * OP_BYTES;
+  static constexpr int STG_BYTES = 32 * 128;        // a staging tile: 32 rows of 128 bytes
+  static constexpr int OFF_BAR = OFF_STG + WARPS * STG_BYTES;
+  // full, empty, tail landed, tail cleared per stage; accumulator full and empty
+  // (2 each); drain; residual landed per epilogue warp
+  static constexpr int NUM_BARS = 4 * STAGES + 5 + WARPS;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = OFF_MISC + 16;
   static constexpr int BYTES = OFF_TAB + (kMaxGroups / kTabStep + 1) * 4;
@@ -56,12 +66,12 @@ struct P16Layout {
 };
 
 template <int EPI>
-__global__ void __launch_bounds__(kP16Threads, 1)
+__global__ void __launch_bounds__(p16_threads(EPI), 1)
     g16_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ CUtensorMap tmap_z,
-                    const G16Args args) {
-  using L = P16Layout;
-  constexpr int S = kP16Stages;
+                    const __grid_constant__ CUtensorMap tmap_r, const G16Args args) {
+  using L = P16Layout<EPI>;
+  constexpr int S = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -84,6 +94,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
   auto accf_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (4 * S + b); };
   auto acce_bar = [&](int b) { return sbase + L::OFF_BAR + 8u * (4 * S + 2 + b); };
   const uint32_t drain_bar = sbase + L::OFF_BAR + 8u * (4 * S + 4);
+  auto res_bar = [&](int w) { return sbase + L::OFF_BAR + 8u * (4 * S + 5 + w); };
   // ragged K: does a stage with `left` of the group's K end inside an MMA's 16,
   // so that the rows behind it have to be cleared?  Such a stage lands on each
   // CTA's own tail barrier, its warp 10 clears the rows and arrives on the
@@ -99,9 +110,10 @@ __global__ void __launch_bounds__(kP16Threads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), 2 * kP16EpiWarps);  // one lane of each epilogue warp of both CTAs, on the leader
+      mbar_init(acce_bar(b), 2 * L::WARPS);  // one lane of each epilogue warp of both CTAs, on the leader
     }
     mbar_init(drain_bar, 1);
+    for (int w = 0; w < L::WARPS; ++w) mbar_init(res_bar(w), 1);
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       tc_commit_pair_multicast(drain_bar, 0x1);
       wait16<false>(drain_bar, 0, nullptr, 100000000ull);
     }
-  } else if (warp == 2 + kP16EpiWarps) {
+  } else if (warp == 2 + L::WARPS) {
     if (ragged_k) {
       // ===== the K rows behind a group's last token belong to the next group:
       // cleared up to the end of the MMAs' last step of 16 in both operands, so
@@ -279,13 +291,22 @@ __global__ void __launch_bounds__(kP16Threads, 1)
     // ===== epilogue: rows of the warp's TMEM lane quarter, one half of the columns
     const int ew = warp - 2;
     const int quarter = warp & 3;
-    const int half = ew >> 2;
+    const int half = ew >> 2;  // which of the column groups
     const uint32_t stg = sbase + L::OFF_STG + ew * L::STG_BYTES;
+    uint32_t res_phase = 0;
     const int h = args.out_type == 1;
     uint32_t it = 0;
     bool ok = true;
     // 32 words of each of the warp's rows through its staging tile (128-byte
     // swizzle); the store before must have read it
+    auto send = [&](const CUtensorMap* map, int x, int y, int z) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(map, stg, x, y, z);
+        bulk_commit_group();
+      }
+    };
     auto put = [&](const CUtensorMap* map, const uint32_t* w, int x, int y, int z) {
       if (lane == 0) bulk_wait_group_read<0>();
       __syncwarp();
@@ -296,12 +317,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
                      "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
                      : "memory");
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_3d(map, stg, x, y, z);
-        bulk_commit_group();
-      }
+      send(map, x, y, z);
     };
     // the accumulator's next buffer is full; false (on every lane) if the wait ran out
     auto wait_full = [&]() -> bool {
@@ -329,13 +345,14 @@ __global__ void __launch_bounds__(kP16Threads, 1)
       g16_k_range(args, tl.group, k0, kn);
       const int row_w = tl.row0 + 128 * static_cast<int>(rank) + 32 * quarter;  // the warp's first row
       const int row = row_w + lane;
-      const int col_w = tl.nb * kP16TN + half * 128;                            // and column
+      constexpr int WCOLS = 1024 / L::WARPS;                                    // columns of a warp
+      const int col_w = tl.nb * kP16TN + half * WCOLS;                          // and column
       const bool valid = row < tl.rows_end;
       const bool mine = row_w < tl.rows_end && col_w < args.n;  // anything to store
       // TMA clips rows behind the tensor's last but not behind a group's
       const bool tma = args.mode != kRaggedM || row_w + 32 <= tl.rows_end;
       const int z_out = args.mode == kRaggedM ? 0 : tl.group;
-      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * WCOLS;
       if constexpr (EPI == kEpiSum) {
         // FP32 sums over a long K: the tensor core's accumulator truncates, so each
         // kP16Seg of K goes into one of its own, and these are added here, rounded
@@ -364,6 +381,101 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             if (col_w + c * 32 < args.n)
               put(&tmap_d, reinterpret_cast<const uint32_t*>(sum) + c * 32, col_w + c * 32, row_w, z_out);
         }
+      } else if constexpr (EPI == kEpiLinear) {
+        // 64 columns a warp, 32 at a time; a pre-activation that is wanted takes a pass
+        // of its own over the accumulator, so that one staging tile does.  The
+        // residual's rows come into the tile by TMA, while the MMAs run if they can, and
+        // the result takes their place.
+        const bool has_res = args.res != nullptr && mine;
+        auto fetch_res = [&]() {
+          if (lane == 0) {
+            bulk_wait_group_read<0>();
+            mbar_arrive_expect_tx(res_bar(ew), L::STG_BYTES);
+            tma_load_3d(stg, &tmap_r, res_bar(ew), col_w, row_w, 0);
+          }
+        };
+        auto load32 = [&](int c, float (&v)[32]) {  // accumulator and bias
+          uint32_t raw[32];
+          tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+          if (args.bias != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (col_w + c + q * 8 < args.n) {
+                float b[8];
+                load8(static_cast<const uint16_t*>(args.bias) + col_w + c + q * 8, args.op_fp16, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[q * 8 + j] += b[j];
+              }
+            }
+          }
+        };
+        auto stage32 = [&](int c, const float (&v)[32]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t at = stg + lane * 128 + (((c / 8 + j) ^ (lane & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack16(v[8 * j], v[8 * j + 1], h)),
+                         "r"(pack16(v[8 * j + 2], v[8 * j + 3], h)), "r"(pack16(v[8 * j + 4], v[8 * j + 5], h)),
+                         "r"(pack16(v[8 * j + 6], v[8 * j + 7], h))
+                         : "memory");
+          }
+        };
+        if (has_res && args.z == nullptr) fetch_res();
+        ok = wait_full();
+        if (!ok) break;
+        if (mine && args.z != nullptr) {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            float v[32];
+            load32(c, v);
+            stage32(c, v);
+          }
+          send(&tmap_z, col_w, row_w, 0);
+          if (has_res) fetch_res();
+        }
+        if (has_res) {
+          ok = wait16<false>(res_bar(ew), res_phase, abort_flag, args.wait_ns);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) {
+            if (lane == 0) {
+              report(args.status, 0x4);
+              *abort_flag = 1;
+            }
+            break;
+          }
+          res_phase ^= 1u;
+        } else {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          if (mine) {
+            float v[32];
+            load32(c, v);
+            uint4 res[4];
+            if (has_res) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t from = stg + lane * 128 + (((c / 8 + q) ^ (lane & 7)) << 4);
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(res[q].x), "=r"(res[q].y), "=r"(res[q].z), "=r"(res[q].w)
+                             : "r"(from)
+                             : "memory");
+              }
+            }
+            if (c == 32) release();
+            g16_activate<32>(args, v, res);
+            stage32(c, v);
+          } else if (c == 32) {
+            release();
+          }
+        }
+        if (mine) send(&tmap_d, col_w, row_w, 0);
       } else {
         ok = wait_full();
         if (!ok) break;
@@ -376,8 +488,10 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             continue;
           }
           uint4 res[8], low[8];
-          if constexpr (EPI != kEpiPlain) g16_load_res<64>(args, args.res, tl.group, row, col0, args.n, valid, res);
-          if constexpr (EPI == kEpiPoly) g16_load_res<64>(args, args.res_lo, tl.group, row, col0, args.n, valid, low);
+          if constexpr (EPI == kEpiPoly) {
+            g16_load_res<64>(args, args.res, tl.group, row, col0, args.n, valid, res);
+            g16_load_res<64>(args, args.res_lo, tl.group, row, col0, args.n, valid, low);
+          }
           float v[64];
           {
             uint32_t raw[2][32];
@@ -398,23 +512,7 @@ __global__ void __launch_bounds__(kP16Threads, 1)
             for (int j = 0; j < 32; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
             put(map, w, col0, row_w, z_out);
           };
-          if constexpr (EPI == kEpiLinear) {
-            if (args.bias != nullptr) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                if (col0 + q * 8 < args.n) {
-                  float b[8];
-                  load8(static_cast<const uint16_t*>(args.bias) + col0 + q * 8, args.op_fp16, b);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) v[q * 8 + j] += b[j];
-                }
-              }
-            }
-            if (args.z != nullptr) put64(&tmap_z);
-            g16_activate<64>(args, v, res);
-          } else {
-            g16_epilogue<EPI, 64>(args, v, res, low, nullptr, tl.group, row, col0, scale);
-          }
+          g16_epilogue<EPI, 64>(args, v, res, low, nullptr, tl.group, row, col0, scale);
           if (tma)
             put64(&tmap_d);
           else if (valid)
@@ -832,16 +930,16 @@ static cudaLaunchConfig_t g16_config(int64_t ctas, int threads, int smem, int cl
 
 template <int EPI>
 static cudaError_t launch_pair16(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
-                                 const CUtensorMap& tz, const G16Args& a, int64_t tiles, int num_sms,
-                                 cudaStream_t stream) {
+                                 const CUtensorMap& tz, const CUtensorMap& tr, const G16Args& a, int64_t tiles,
+                                 int num_sms, cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow_smem(g16_pair_kernel<EPI>, P16Layout::ALLOC, done);
+  cudaError_t e = allow_smem(g16_pair_kernel<EPI>, P16Layout<EPI>::ALLOC, done);
   if (e != cudaSuccess) return e;
   const int64_t most = num_sms / 2;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
-      g16_config(2 * (tiles < most ? tiles : most), kP16Threads, P16Layout::ALLOC, 2, stream, attr);
-  return cudaLaunchKernelEx(&cfg, g16_pair_kernel<EPI>, ta, tb, td, tz, a);
+      g16_config(2 * (tiles < most ? tiles : most), p16_threads(EPI), P16Layout<EPI>::ALLOC, 2, stream, attr);
+  return cudaLaunchKernelEx(&cfg, g16_pair_kernel<EPI>, ta, tb, td, tz, tr, a);
 }
 
 // Clusters of `splits` CTAs that the GPU holds at once with one CTA to an SM
@@ -995,7 +1093,7 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
 
   const int64_t a_depth = p.mode == kBatched ? p.groups : 1;
   const int64_t b_depth = a.b_per_group ? p.groups : 1;
-  CUtensorMap ta, tb, td = {}, tz = {};
+  CUtensorMap ta, tb, td = {}, tz = {}, tr = {};
   if (!make_operand16(&ta, p.a, p.a_mn, a.a_wide, p.m, p.k, a_depth, p.a_ld, p.a_batch, small ? 32 : 128) ||
       !make_operand16(&tb, p.b, p.b_mn, a.b_wide, p.n, p.k, b_depth, p.b_ld, p.b_batch, 128))
     return cudaErrorInvalidValue;
@@ -1008,10 +1106,13 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   if (!make_tmap_out16(&td, p.d, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2)) return cudaErrorInvalidValue;
   if (p.z && !make_tmap_out16(&tz, p.z, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2))
     return cudaErrorInvalidValue;
-  if (p.out_type == 2) return launch_pair16<kEpiSum>(ta, tb, td, tz, a, tiles, num_sms, stream);
-  if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, a, tiles, num_sms, stream);
-  if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, a, tiles, num_sms, stream);
-  return launch_pair16<kEpiPlain>(ta, tb, td, tz, a, tiles, num_sms, stream);
+  if (p.epi == kEpiLinear && p.res &&
+      !make_tmap_out16(&tr, const_cast<void*>(p.res), p.n, p.m, 1, p.res_ld, p.m * p.res_ld, false))
+    return cudaErrorInvalidValue;
+  if (p.out_type == 2) return launch_pair16<kEpiSum>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
+  if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
+  if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
+  return launch_pair16<kEpiPlain>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
 }
 
 }  // namespace mxk

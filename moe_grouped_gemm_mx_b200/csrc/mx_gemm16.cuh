@@ -313,12 +313,26 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
+// Phi(z) = erfc(-z / sqrt 2) / 2 by the approximation 7.1.26 of Abramowitz and
+// Stegun, erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2) with t = 1 / (1 + p x), within
+// 1.5e-7.
+__device__ __forceinline__ float normal_cdf_f32(float z) {
+  const float x = fabsf(z) * 0.7071067811865476f;
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float half = 0.5f * p * t * __expf(-x * x);  // Phi(-|z|)
+  return z >= 0.0f ? 1.0f - half : half;
+}
+
 // act(z); 0.5 (1 + tanh u) = sigmoid(2 u).  relu keeps a NaN.
 __device__ __forceinline__ float act_f32(float z, int act) {
   switch (act) {
     case 1: return z < 0.0f ? 0.0f : z;
     case 2: return z * sigmoid_f32(z);
-    case 3: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case 3: return z * normal_cdf_f32(z);
     case 4: return z * sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
     default: return z;
   }
