@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
       for (int t = pair; t < total && ok; t += npairs) {
         int k0, kn;
         g16_k_range(args, g16_decode<kP16TM>(args, tab, t).group, k0, kn);
+        if (kn == 0) continue;  // the epilogue writes zeros by itself
         int kk = 0;
         do {
           const uint32_t buf = it & 1u;
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
     const int half = ew >> 2;  // which of the column groups
     const uint32_t stg = sbase + L::OFF_STG + ew * L::STG_BYTES;
     uint32_t res_phase = 0;
+    bool zeros = false;  // the staging tile holds zeros
     const int h = args.out_type == 1;
     uint32_t it = 0;
     bool ok = true;
@@ -353,24 +355,45 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
       const bool tma = args.mode != kRaggedM || row_w + 32 <= tl.rows_end;
       const int z_out = args.mode == kRaggedM ? 0 : tl.group;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * WCOLS;
+      if constexpr (EPI == kEpiPlain || EPI == kEpiSum) {
+        if (kn == 0) {  // a group without tokens: zeros from the staging tile, no accumulator
+          if (mine) {
+            if (!zeros) {
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stg + j * 512 + lane * 16), "r"(0) : "memory");
+              fence_proxy_async_smem();
+              __syncwarp();
+              zeros = true;
+            }
+            if (lane == 0) {
+              constexpr int COLS = EPI == kEpiSum ? 32 : 64;
+              for (int c = 0; c < WCOLS && col_w + c < args.n; c += COLS) tma_store_3d(&tmap_d, stg, col_w + c, row_w, z_out);
+              bulk_commit_group();
+            }
+          }
+          continue;
+        }
+        zeros = false;
+      }
       if constexpr (EPI == kEpiSum) {
         // FP32 sums over a long K: the tensor core's accumulator truncates, so each
         // kP16Seg of K goes into one of its own, and these are added here, rounded
         float sum[128];
 #pragma unroll
         for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-        for (int kk = 0; ok && (kk == 0 || kk < kn); kk += kP16Seg) {
+        for (int kk = 0; kk < kn; kk += kP16Seg) {
           ok = wait_full();
           if (!ok) break;
-          if (kn > 0) {  // no MMA wrote an empty sum
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t raw[16];
-              tc_ld_32x32b_x16(t_row + (it & 1u) * kP16TN + c * 16, raw);
-              tc_wait_ld();
+          for (int c = 0; c < 8; ++c) {
+            uint32_t raw[16];
+            tc_ld_32x32b_x16(t_row + (it & 1u) * kP16TN + c * 16, raw);
+            tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(raw[j]);
-            }
+            for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(raw[j]);
           }
           release();
         }
@@ -502,10 +525,6 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
             for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j / 32][j % 32]);
           }
           if (c == 64) release();
-          if (kn == 0) {  // no MMA wrote an empty sum
-#pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
-          }
           auto put64 = [&](const CUtensorMap* map) {
             uint32_t w[32];
 #pragma unroll
