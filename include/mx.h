@@ -505,7 +505,8 @@ mx_status mx_linear_act(const void *x, const void *w, const void *bias, const vo
  * nullable: not wanted.  With an activation, z and dz [m, n] (out; rounded to
  * `dtype` for the two products) are needed; without one both may be NULL and dy
  * takes dz's place.  dbias sums the unrounded products in FP32 in a fixed order;
- * it needs `workspace` of mx_linear_act_backward_workspace_bytes(m, n) bytes.
+ * it needs `workspace` of mx_linear_act_backward_workspace_bytes(m, n) bytes (none
+ * up to m = 1024).
  * ReLU's derivative at zero is 0.  x is read for dw only, w for dx only (NULL
  * otherwise).  m == 0 gives zero dw and dbias; n == 0 gives zero dx.
  */

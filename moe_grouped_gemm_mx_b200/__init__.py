@@ -905,31 +905,32 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
     if (x is None and dw is not None) or (w is None and dx is not None):
         raise ValueError("dw needs x, dx needs w")
     for t, nm in ((x, "x"), (w, "w")):
-        if t is not None:
-            _operand16(t, nm, 2)
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 2):
+            raise ValueError(f"{nm} must be a 2-D torch.Tensor")
     k = x.shape[1] if x is not None else w.shape[1]
     if act != 0 and z is None:
         raise ValueError(f"activation {activation!r} needs z")
     for t, nm, shape in ((x, "x", (m, k)), (w, "w", (n, k)), (z, "z", (m, n))):
         if t is not None:
             _check16(t, nm, shape, dt, dev)
-    need = mx_linear_act_backward_workspace_bytes(m, n)
+    for t, nm, shape in ((dx, "dx", (m, k)), (dw, "dw", (n, k)), (dbias, "dbias", (n,)), (dz, "dz", (m, n))):
+        if t is not None:
+            _check16(t, nm, shape, dt, dev)
+    if workspace is not None:
+        _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     with _launch_on(dy, stream) as s:
         if w is not None and dx is None:
-            dx = torch.empty((m, k), dtype=dt, device=dev)
+            dx = dy.new_empty((m, k))
         if x is not None and dw is None:
-            dw = torch.empty((n, k), dtype=dt, device=dev)
+            dw = dy.new_empty((n, k))
         if bias_grad and dbias is None:
-            dbias = torch.empty(n, dtype=dt, device=dev)
+            dbias = dy.new_empty(n)
         if act != 0 and dz is None:
-            dz = torch.empty((m, n), dtype=dt, device=dev)
-        if dbias is not None and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        for t, nm, shape in ((dx, "dx", (m, k)), (dw, "dw", (n, k)), (dbias, "dbias", (n,)), (dz, "dz", (m, n))):
-            if t is not None:
-                _check16(t, nm, shape, dt, dev)
-        if workspace is not None:
-            _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+            dz = dy.new_empty((m, n))
+        if dbias is not None and workspace is None and m > 0 and n > 0:
+            need = mx_linear_act_backward_workspace_bytes(m, n)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         _raise(_lib.mx_linear_act_backward(_ptr(dy), _ptr(z), _ptr(x), _ptr(w), _ptr(dz), _ptr(dx), _ptr(dw),
                                            _ptr(dbias), m, n, k, _DTYPES[dt], act, _ptr(workspace),
                                            0 if workspace is None else workspace.numel(),

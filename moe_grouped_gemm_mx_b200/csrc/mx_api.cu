@@ -696,7 +696,8 @@ mx_status mx_linear_act(const void* x, const void* w, const void* bias, const vo
 
 size_t mx_linear_act_backward_workspace_bytes(int64_t m, int64_t n) {
   if (m <= 0 || n <= 0) return 0;
-  return static_cast<size_t>(mxk::act_backward_chunks(m) * n) * sizeof(float);
+  const int64_t chunks = mxk::act_backward_chunks(m);
+  return chunks == 1 ? 0 : static_cast<size_t>(chunks * n) * sizeof(float);
 }
 
 mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, const void* w, void* dz, void* dx,
@@ -712,8 +713,8 @@ mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, c
     return st;
   }
   if (!dy || (dx && !w) || (dw && !x) || (act != MX_ACT_NONE && (!z || !dz))) return MX_ERR_INVALID_ARGUMENT;
-  if (dbias && (!workspace || workspace_bytes < mx_linear_act_backward_workspace_bytes(m, n)))
-    return MX_ERR_INVALID_ARGUMENT;
+  const size_t needed = dbias ? mx_linear_act_backward_workspace_bytes(m, n) : 0;
+  if (needed > 0 && (!workspace || workspace_bytes < needed)) return MX_ERR_INVALID_ARGUMENT;
   if (!dx && !dw && !dbias) return MX_OK;
   int sms;
   int32_t* status;
@@ -724,8 +725,14 @@ mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, c
   if (act != MX_ACT_NONE || dbias)
     e = mxk::launch_act_backward(dy, z, dz, dbias, static_cast<float*>(workspace), m, n, act, dtype == MX_FP16, s);
   const void* g = act != MX_ACT_NONE ? dz : dy;
-  if (e == cudaSuccess && dx) e = mxk::launch_gemm16(dense16(g, 0, w, 1, dx, m, k, n, dtype, status), sms, s);
-  if (e == cudaSuccess && dw) e = mxk::launch_gemm16(dense16(g, 1, x, 1, dw, n, k, m, dtype, status), sms, s);
+  const mxk::Gemm16 gx = dense16(g, 0, w, 1, dx, m, k, n, dtype, status);
+  const mxk::Gemm16 gw = dense16(g, 1, x, 1, dw, n, k, m, dtype, status);
+  if (e == cudaSuccess && dx && dw) {
+    e = mxk::launch_gemm16_two(gx, gw, sms, s);
+  } else {
+    if (e == cudaSuccess && dx) e = mxk::launch_gemm16(gx, sms, s);
+    if (e == cudaSuccess && dw) e = mxk::launch_gemm16(gw, sms, s);
+  }
   return from_cuda(e);
 }
 

@@ -588,10 +588,10 @@ struct S16Layout {
   static_assert((STAGES <= 3 ? 2 : 1) * ALLOC <= 232448, "shared memory budget");
 };
 
+// One CTA's part of a product: `cta` counts from the product's first CTA.
 template <int EPI, int STAGES>
-__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
-    g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                     const G16Args args) {
+__device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const CUtensorMap* tmap_b, const G16Args& args,
+                                              const int cta) {
   using L = S16Layout<STAGES>;
   constexpr int S = STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int splits = args.splits;
-  const int tile = static_cast<int>(blockIdx.x) / splits;
-  const int part = static_cast<int>(blockIdx.x) - tile * splits;  // also the rank in the cluster
+  const int tile = cta / splits;
+  const int part = cta - tile * splits;  // also the rank in the cluster
 
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile uint32_t* tmem_slot = misc + 0;
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
     *abort_flag = 0;
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmap_a);
-    prefetch_tmap(&tmap_b);
+    prefetch_tmap(tmap_a);
+    prefetch_tmap(tmap_b);
   }
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   int total;
   if (args.mode == kRaggedM) {
     const int bad = __syncthreads_or(g16_offsets_bad(args, args.m));
-    if (bad && threadIdx.x == 0 && blockIdx.x == 0) report(args.status, 0x1);
+    if (bad && threadIdx.x == 0 && cta == 0) report(args.status, 0x1);
     if (warp == 0) g16_prefix<kS16T>(args, tab, bad, &misc[2]);
     __syncthreads();
     total = static_cast<int>(misc[2]);
@@ -674,20 +674,20 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
         const uint32_t sb = sbase + L::OFF_B + s * L::OP_BYTES;
         const int kk = c * kS16K;
         if (!args.b_mn) {
-          tma_load_3d(sb, &tmap_b, full_bar(s), kk, col0, b_z);
+          tma_load_3d(sb, tmap_b, full_bar(s), kk, col0, b_z);
         } else if (args.b_wide) {
-          tma_load_4d(sb, &tmap_b, full_bar(s), 0, kk, col0 / 64, b_z);
+          tma_load_4d(sb, tmap_b, full_bar(s), 0, kk, col0 / 64, b_z);
         } else {
-          tma_load_3d(sb, &tmap_b, full_bar(s), col0, kk, b_z);
-          tma_load_3d(sb + 8192, &tmap_b, full_bar(s), col0 + 64, kk, b_z);
+          tma_load_3d(sb, tmap_b, full_bar(s), col0, kk, b_z);
+          tma_load_3d(sb + 8192, tmap_b, full_bar(s), col0 + 64, kk, b_z);
         }
         if (!args.a_mn) {
-          for (int b = 0; b < a_boxes; ++b) tma_load_3d(sa + b * 4096, &tmap_a, full_bar(s), kk, tl.row0 + b * 32, a_z);
+          for (int b = 0; b < a_boxes; ++b) tma_load_3d(sa + b * 4096, tmap_a, full_bar(s), kk, tl.row0 + b * 32, a_z);
         } else if (args.a_wide) {
-          tma_load_4d(sa, &tmap_a, full_bar(s), 0, kk, tl.row0 / 64, a_z);
+          tma_load_4d(sa, tmap_a, full_bar(s), 0, kk, tl.row0 / 64, a_z);
         } else {
-          tma_load_3d(sa, &tmap_a, full_bar(s), tl.row0, kk, a_z);
-          tma_load_3d(sa + 8192, &tmap_a, full_bar(s), tl.row0 + 64, kk, a_z);
+          tma_load_3d(sa, tmap_a, full_bar(s), tl.row0, kk, a_z);
+          tma_load_3d(sa + 8192, tmap_a, full_bar(s), tl.row0 + 64, kk, a_z);
         }
         if (++s == S) { s = 0; phase ^= 1u; }
       }
@@ -857,6 +857,32 @@ __global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
   }
 }
 
+template <int EPI, int STAGES>
+__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
+    g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                     const __grid_constant__ G16Args args) {
+  g16_small_cta<EPI, STAGES>(&tmap_a, &tmap_b, args, static_cast<int>(blockIdx.x));
+}
+
+// Two independent products of plain epilogue in one launch, the first's CTAs
+// before the second's, K split alike (a layer's two gradients: neither fills the
+// GPU, and the second's launch costs as much as its work).
+struct G16Two {
+  G16Args first, second;
+  int first_ctas;
+};
+
+template <int STAGES>
+__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
+    g16_two_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
+                   const __grid_constant__ CUtensorMap a2, const __grid_constant__ CUtensorMap b2,
+                   const __grid_constant__ G16Two two) {
+  const int cta = static_cast<int>(blockIdx.x);
+  const bool second = cta >= two.first_ctas;
+  g16_small_cta<kEpiPlain, STAGES>(second ? &a2 : &a1, second ? &b2 : &b1, second ? two.second : two.first,
+                                   second ? cta - two.first_ctas : cta);
+}
+
 // ======================================================================= host
 
 // 16-bit operand [depth, rows, cols] (cols contiguous, rows `ld` elements
@@ -1014,61 +1040,91 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     0.51 us where two share one; the first six chunks 0.15 us more each, and
 //     2.5 us for every further round (64x2112x7168 by 4: 12.9 estimated, 12.9
 //     measured; by 2: 19.5, 19.7; 1037x7168x2048 whole: 42, 38.7).
-static bool pick_small(const Gemm16& p, int num_sms, int* splits) {
-  *splits = 1;
-  if (p.mode == kRaggedK || p.out_type == 2) return false;  // neither clears rows behind a group nor sums in parts
-  const int64_t chunks = ceil_div(p.k, kS16K);
+struct G16Tiles {
+  double pair, small;  // 256 x 256 and 128 x 128 tiles to do
+  int64_t chunks;      // of 64 of K
+};
+
+static G16Tiles count_tiles(const Gemm16& p) {
   const double np = static_cast<double>(ceil_div(p.n, kP16TN)), ns = static_cast<double>(ceil_div(p.n, kS16T));
-  double tiles_p, tiles_s;
+  G16Tiles c;
+  c.chunks = ceil_div(p.k, kS16K);
   if (p.mode == kRaggedM) {
     // the groups' sizes are on the device: the mean size, with half a tile more for each group's end
     const double groups = static_cast<double>(p.m < p.groups ? p.m : p.groups), rows = static_cast<double>(p.m) / groups;
-    tiles_p = groups * std::fmax(1.0, rows / kP16TM + 0.5) * np;
-    tiles_s = groups * std::fmax(1.0, rows / kS16T + 0.5) * ns;
+    c.pair = groups * std::fmax(1.0, rows / kP16TM + 0.5) * np;
+    c.small = groups * std::fmax(1.0, rows / kS16T + 0.5) * ns;
   } else {
     const double entries = static_cast<double>(p.groups);
     const double mp = static_cast<double>(ceil_div(p.m, kP16TM)), ms = static_cast<double>(ceil_div(p.m, kS16T));
-    tiles_p = entries * (p.sym ? mp * (mp + 1) / 2 : mp * np);
-    tiles_s = entries * (p.sym ? ms * (ms + 1) / 2 : ms * ns);
+    c.pair = entries * (p.sym ? mp * (mp + 1) / 2 : mp * np);
+    c.small = entries * (p.sym ? ms * (ms + 1) / 2 : ms * ns);
   }
-  const double cost_pair = 8.0 + 0.3 * std::ceil(tiles_p / (num_sms / 2)) * static_cast<double>(chunks);
+  return c;
+}
+
+static double pair_cost(const G16Tiles& c, int num_sms) {
+  return 8.0 + 0.3 * std::ceil(c.pair / (num_sms / 2)) * static_cast<double>(c.chunks);
+}
+
+// The small kernel's cost on `tiles` tiles, the longest of `chunks`, and the best
+// split, at most one CTA per chunk of the product with the fewest.
+static double small_cost(double tiles, int64_t chunks, int64_t fewest, int num_sms, int* splits) {
   double best = 1e30;
+  *splits = 1;
   for (int s = 1; s <= 8; s *= 2) {
-    if (s > chunks || (s > 1 && tiles_s * s > 2.0 * num_sms)) break;
+    if (s > fewest || (s > 1 && tiles * s > 2.0 * num_sms)) break;
     const double each = static_cast<double>(ceil_div(chunks, s));
-    const double exchange = s == 1 ? 0.0 : s == 2 ? 0.6 : s == 4 ? 1.0 : 1.3 + 0.2 * tiles_s;
-    const double rounds = std::ceil(tiles_s * s / (2.0 * num_sms));
+    const double exchange = s == 1 ? 0.0 : s == 2 ? 0.6 : s == 4 ? 1.0 : 1.3 + 0.2 * tiles;
+    const double rounds = std::ceil(tiles * s / (2.0 * num_sms));
     double cost = 4.0 + exchange + 0.15 * std::fmin(each, 6.0);
-    if (tiles_s <= static_cast<double>(lone_clusters(s, num_sms)))
+    if (tiles <= static_cast<double>(lone_clusters(s, num_sms)))
       cost += 0.25 * each;
     else
-      cost += (tiles_s * s <= num_sms ? 0.39 : 0.51) * each * rounds + 2.5 * (rounds - 1.0);
+      cost += (tiles * s <= num_sms ? 0.39 : 0.51) * each * rounds + 2.5 * (rounds - 1.0);
     if (cost < best) {
       best = cost;
       *splits = s;
     }
   }
-  return best < cost_pair;
+  return best;
 }
 
-cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
-  int splits = 1;
-  bool small = pick_small(p, num_sms, &splits);
+static bool small_can(const Gemm16& p) {
+  return p.mode != kRaggedK && p.out_type != 2;  // it neither clears rows behind a group nor sums in parts
+}
+
+struct G16Choice {
+  bool small;
+  int splits;
+};
+
+static G16Choice choose(const Gemm16& p, int num_sms) {
+  G16Choice c = {false, 1};
   // MX_GEMM16_CONFIG forces a kernel for tests and tuning: 0 the pair kernel, 1,
   // 2, 4 or 8 the small one with that many CTAs (at most one per K chunk) a tile
   if (const char* forced = std::getenv("MX_GEMM16_CONFIG")) {
     const int v = std::atoi(forced);
-    if (v == 0) {
-      small = false;
-    } else if (p.mode != kRaggedK && p.out_type != 2 && (v == 1 || v == 2 || v == 4 || v == 8)) {
-      small = true;
-      for (splits = v; splits > ceil_div(p.k, kS16K); splits /= 2) {
+    if (v == 0 || !small_can(p)) return c;
+    if (v == 1 || v == 2 || v == 4 || v == 8) {
+      c.small = true;
+      for (c.splits = v; c.splits > ceil_div(p.k, kS16K); c.splits /= 2) {
       }
+      return c;
     }
   }
-  const int tm = small ? kS16T : kP16TM, tn = small ? kS16T : kP16TN;
+  if (!small_can(p)) return c;
+  const G16Tiles tiles = count_tiles(p);
+  c.small = small_cost(tiles.small, tiles.chunks, tiles.chunks, num_sms, &c.splits) < pair_cost(tiles, num_sms);
+  return c;
+}
 
-  G16Args a = {};
+// Arguments and operand maps of a product on the chosen kernel; *tiles is the most there can be.
+static cudaError_t prepare16(const Gemm16& p, const G16Choice& c, G16Args* args, CUtensorMap* ta, CUtensorMap* tb,
+                             int64_t* tiles) {
+  const int tm = c.small ? kS16T : kP16TM, tn = c.small ? kS16T : kP16TN;
+  G16Args& a = *args;
+  a = {};
   a.bias = p.bias;
   a.res = p.res;
   a.res_lo = p.res_lo;
@@ -1102,21 +1158,29 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   a.out_type = p.out_type;
   a.act = p.act;
   a.sym = p.sym;
-  a.splits = splits;
+  a.splits = c.splits;
 
-  // the most tiles there can be (ragged M: every group adds at most one part tile a column)
-  const int64_t tiles = p.mode == kRaggedM ? (p.m / tm + p.groups) * a.n_tiles
-                                           : p.groups * (p.sym ? static_cast<int64_t>(a.m_tiles) * (a.m_tiles + 1) / 2
-                                                               : static_cast<int64_t>(a.m_tiles) * a.n_tiles);
-  if (tiles * splits > 0x3FFFFFFFll) return cudaErrorInvalidValue;  // tile numbers are 32-bit
-
+  // (ragged M: every group adds at most one part tile a column)
+  *tiles = p.mode == kRaggedM ? (p.m / tm + p.groups) * a.n_tiles
+                              : p.groups * (p.sym ? static_cast<int64_t>(a.m_tiles) * (a.m_tiles + 1) / 2
+                                                  : static_cast<int64_t>(a.m_tiles) * a.n_tiles);
+  if (*tiles * c.splits > 0x3FFFFFFFll) return cudaErrorInvalidValue;  // tile numbers are 32-bit
   const int64_t a_depth = p.mode == kBatched ? p.groups : 1;
   const int64_t b_depth = a.b_per_group ? p.groups : 1;
-  CUtensorMap ta, tb, td = {}, tz = {}, tr = {};
-  if (!make_operand16(&ta, p.a, p.a_mn, a.a_wide, p.m, p.k, a_depth, p.a_ld, p.a_batch, small ? 32 : 128) ||
-      !make_operand16(&tb, p.b, p.b_mn, a.b_wide, p.n, p.k, b_depth, p.b_ld, p.b_batch, 128))
+  if (!make_operand16(ta, p.a, p.a_mn, a.a_wide, p.m, p.k, a_depth, p.a_ld, p.a_batch, c.small ? 32 : 128) ||
+      !make_operand16(tb, p.b, p.b_mn, a.b_wide, p.n, p.k, b_depth, p.b_ld, p.b_batch, 128))
     return cudaErrorInvalidValue;
-  if (small) {
+  return cudaSuccess;
+}
+
+cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
+  const G16Choice c = choose(p, num_sms);
+  G16Args a;
+  CUtensorMap ta, tb, td = {}, tz = {}, tr = {};
+  int64_t tiles = 0;
+  const cudaError_t e = prepare16(p, c, &a, &ta, &tb, &tiles);
+  if (e != cudaSuccess) return e;
+  if (c.small) {
     if (p.epi == kEpiLinear) return launch_small16<kEpiLinear>(ta, tb, a, tiles, num_sms, stream);
     if (p.epi == kEpiPoly) return launch_small16<kEpiPoly>(ta, tb, a, tiles, num_sms, stream);
     return launch_small16<kEpiPlain>(ta, tb, a, tiles, num_sms, stream);
@@ -1132,6 +1196,40 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   return launch_pair16<kEpiPlain>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
+}
+
+// Two products of plain epilogue, neither of which the other reads: one launch
+// where the small kernel does both sooner than two.
+cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cudaStream_t stream) {
+  const G16Tiles tp = count_tiles(p), tq = count_tiles(q);
+  int sp = 1, sq = 1, s = 1;
+  const double apart = std::fmin(small_cost(tp.small, tp.chunks, tp.chunks, num_sms, &sp), pair_cost(tp, num_sms)) +
+                       std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, num_sms, &sq), pair_cost(tq, num_sms));
+  const int64_t longest = tp.chunks > tq.chunks ? tp.chunks : tq.chunks, fewest = tp.chunks < tq.chunks ? tp.chunks : tq.chunks;
+  const bool together = p.mode == kBatched && q.mode == kBatched && p.epi == kEpiPlain && q.epi == kEpiPlain && small_can(p) &&
+                        small_can(q) && std::getenv("MX_GEMM16_CONFIG") == nullptr &&
+                        small_cost(tp.small + tq.small, longest, fewest, num_sms, &s) < apart;
+  if (!together) {
+    const cudaError_t e = launch_gemm16(p, num_sms, stream);
+    return e != cudaSuccess ? e : launch_gemm16(q, num_sms, stream);
+  }
+  const G16Choice c = {true, s};
+  G16Two two = {};
+  CUtensorMap a1, b1, a2, b2;
+  int64_t t1 = 0, t2 = 0;
+  cudaError_t e = prepare16(p, c, &two.first, &a1, &b1, &t1);
+  if (e == cudaSuccess) e = prepare16(q, c, &two.second, &a2, &b2, &t2);
+  if (e != cudaSuccess) return e;
+  two.first_ctas = static_cast<int>(t1 * s);
+  const bool lone = t1 + t2 <= lone_clusters(s, num_sms);
+  static std::atomic<bool> done3[kMaxDevices], done6[kMaxDevices];
+  e = lone ? allow_smem(g16_two_kernel<6>, S16Layout<6>::ALLOC, done6) : allow_smem(g16_two_kernel<3>, S16Layout<3>::ALLOC, done3);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg =
+      g16_config((t1 + t2) * s, kS16Threads, lone ? S16Layout<6>::ALLOC : S16Layout<3>::ALLOC, s, stream, attr);
+  return lone ? cudaLaunchKernelEx(&cfg, g16_two_kernel<6>, a1, b1, a2, b2, two)
+              : cudaLaunchKernelEx(&cfg, g16_two_kernel<3>, a1, b1, a2, b2, two);
 }
 
 }  // namespace mxk

@@ -104,6 +104,8 @@ struct Gemm16 {
   int scale_pow = 1;
 };
 cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream);
+// Two independent plain products, in one launch where that is sooner.
+cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cudaStream_t stream);
 
 // dz = dy * act'(z) and, with dbias, its column sums (mx_act.cu); partial:
 // act_backward_chunks(m) * n floats, needed with dbias.

@@ -35,7 +35,7 @@ def test_linear_act(lib):
 def test_linear_act_backward(lib):
     ws = lib.mx_linear_act_backward_workspace_bytes
     assert ws(0, 8) == ws(8, 0) == ws(-1, 8) == 0
-    assert ws(1, 8) == ws(1024, 8) == 32 and ws(1025, 8) == 9 * 32 and ws(8192, 4096) == 64 * 4096 * 4
+    assert ws(1, 8) == ws(1024, 8) == 0 and ws(1025, 8) == 9 * 32 and ws(8192, 4096) == 64 * 4096 * 4
 
     def f(dy=FAKE, z=FAKE, x=FAKE, w=FAKE, dz=FAKE, dx=FAKE, dw=FAKE, db=FAKE, m=4, n=16, k=32, dtype=BF16, act=1, work=FAKE,
           size=1 << 20):
@@ -44,7 +44,8 @@ def test_linear_act_backward(lib):
     assert f(k=0) == f(k=33) == f(n=9) == f(m=BIG) == MX_ERR_UNSUPPORTED_SHAPE
     assert f(dy=None) == f(z=None) == f(dz=None) == MX_ERR_INVALID_ARGUMENT
     assert f(x=None) == f(w=None) == MX_ERR_INVALID_ARGUMENT            # dw wants x, dx wants w
-    assert f(work=None) == f(size=16 * 4 - 1) == MX_ERR_INVALID_ARGUMENT  # dbias wants the workspace
+    big = {"m": 2000, "n": 16}
+    assert f(work=None, **big) == f(size=16 * 16 * 4 - 1, **big) == MX_ERR_INVALID_ARGUMENT  # dbias wants the workspace
     for name in ("dy", "z", "x", "w", "dz", "dx", "dw", "db", "work"):
         assert f(**{name: FAKE + 4}) == MX_ERR_MISALIGNED
     assert f(dx=None, dw=None, db=None) == MX_OK                        # nothing wanted

@@ -354,5 +354,5 @@ def test_python_refusals(mx):
     with pytest.raises(ValueError):
         mx.mx_linear_act_backward(normal((16, 32), BF16, 3), x, w, activation="relu")  # no z
     with pytest.raises(mx.MXError):
-        mx.mx_linear_act_backward(normal((16, 32), BF16, 3), x, w, bias_grad=True,
+        mx.mx_linear_act_backward(normal((1100, 32), BF16, 3), normal((1100, 64), BF16, 1), w, bias_grad=True,
                                   workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
