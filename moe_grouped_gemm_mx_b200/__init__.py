@@ -778,38 +778,32 @@ def mx_moe_combine_peer(y_ptrs: torch.Tensor, y_rows: int, n: int, src_rank: tor
 
 # ---------------------------------------------------------------- 16-bit products
 
-class _launch_on:
-    """The device of ``t`` and the stream the call runs on, both made current,
-    so that what the call allocates belongs to that stream.  Where they are
-    already (the usual call) nothing is switched."""
-
-    __slots__ = ("contexts", "pointer")
-
-    def __init__(self, t: torch.Tensor, stream):
-        index = t.get_device()
-        self.contexts = ()
-        if stream is None and index == torch.cuda.current_device():
-            self.pointer = torch._C._cuda_getCurrentRawStream(index)
-            return
-        device = torch.cuda.device(index)
-        if stream is None:
-            self.contexts = (device,)
-            self.pointer = torch._C._cuda_getCurrentRawStream(index)
-            return
+def _begin(t: torch.Tensor, stream):
+    """(stream pointer, contexts): the device of ``t`` and the stream the call
+    runs on, made current so that what the call allocates belongs to that
+    stream; ``_end(contexts)`` goes back.  Where they are current already (the
+    usual call) there is nothing to switch and contexts is None."""
+    index = t.get_device()
+    if stream is None and index == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(index), None
+    if stream is None:
+        contexts = [torch.cuda.device(index)]
+        pointer = torch._C._cuda_getCurrentRawStream(index)
+    else:
         s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device)
         if s.device != t.device:
             raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
-        self.contexts = (device, torch.cuda.stream(s))
-        self.pointer = s.cuda_stream
+        contexts = [torch.cuda.device(index), torch.cuda.stream(s)]
+        pointer = s.cuda_stream
+    for c in contexts:
+        c.__enter__()
+    return pointer, contexts
 
-    def __enter__(self) -> int:
-        for c in self.contexts:
-            c.__enter__()
-        return self.pointer
 
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+def _end(contexts):
+    if contexts is not None:
+        for c in reversed(contexts):
+            c.__exit__(None, None, None)
 
 
 def _check16(t: torch.Tensor, name: str, shape, dtype, device):
@@ -866,16 +860,24 @@ def mx_linear_act(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = 
     n = w.shape[0]
     dev = x.device
     _check16(w, "w", (n, k), dt, dev)
-    for t, nm, shape in ((bias, "bias", (n,)), (residual, "residual", (m, n)), (z, "z", (m, n)), (y, "y", (m, n))):
-        if t is not None:
-            _check16(t, nm, shape, dt, dev)
-    with _launch_on(x, stream) as s:
+    if bias is not None:
+        _check16(bias, "bias", (n,), dt, dev)
+    if residual is not None:
+        _check16(residual, "residual", (m, n), dt, dev)
+    if z is not None:
+        _check16(z, "z", (m, n), dt, dev)
+    if y is not None:
+        _check16(y, "y", (m, n), dt, dev)
+    s, contexts = _begin(x, stream)
+    try:
         if y is None:
             y = x.new_empty((m, n))
         if return_z and z is None:
             z = x.new_empty((m, n))
         _raise(_lib.mx_linear_act(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(z), _ptr(y), m, n, k, _DTYPES[dt],
                                   act, _status_on(dev_status, dev), s), "mx_linear_act")
+    finally:
+        _end(contexts)
     return y if z is None else (y, z)
 
 
@@ -918,7 +920,8 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
             _check16(t, nm, shape, dt, dev)
     if workspace is not None:
         _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
-    with _launch_on(dy, stream) as s:
+    s, contexts = _begin(dy, stream)
+    try:
         if w is not None and dx is None:
             dx = dy.new_empty((m, k))
         if x is not None and dw is None:
@@ -935,6 +938,8 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
                                            _ptr(dbias), m, n, k, _DTYPES[dt], act, _ptr(workspace),
                                            0 if workspace is None else workspace.numel(),
                                            _status_on(dev_status, dev), s), "mx_linear_act_backward")
+    finally:
+        _end(contexts)
     return dx, dw, dbias
 
 
@@ -950,17 +955,23 @@ def mx_grouped_gemm_ragged(a: torch.Tensor, b: torch.Tensor, group_offsets: torc
     d [M_total, N] with d[i] = a[i] b[e]^T for the rows of expert e.  Rows
     outside [offsets[0], offsets[E]) are left as they were."""
     dt = _operand16(a, "a", 2)
-    _operand16(b, "b", 3)
+    if not isinstance(b, torch.Tensor) or b.dim() != 3:
+        raise ValueError("b must be a 3-D torch.Tensor")
     m, k = a.shape
     groups, n = b.shape[0], b.shape[1]
     dev = a.device
     _check16(b, "b", (groups, n, k), dt, dev)
     _offsets(group_offsets, groups, dev)
-    with _launch_on(a, stream) as s:
-        d = torch.empty((m, n), dtype=dt, device=dev) if d is None else d
-        _check16(d, "d", (m, n), dt, dev)
+    s, contexts = _begin(a, stream)
+    try:
+        if d is None:
+            d = a.new_empty((m, n))
+        else:
+            _check16(d, "d", (m, n), dt, dev)
         _raise(_lib.mx_grouped_gemm_ragged(_ptr(a), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt], _ptr(d),
                                            _status_on(dev_status, dev), s), "mx_grouped_gemm_ragged")
+    finally:
+        _end(contexts)
     return d
 
 
@@ -971,18 +982,24 @@ def mx_grouped_gemm_ragged_dgrad(dd: torch.Tensor, b: torch.Tensor, group_offset
     da [M_total, K] with da[i] = dd[i] b[e].  Rows outside the groups are left
     as they were."""
     dt = _operand16(dd, "dd", 2)
-    _operand16(b, "b", 3)
+    if not isinstance(b, torch.Tensor) or b.dim() != 3:
+        raise ValueError("b must be a 3-D torch.Tensor")
     m, n = dd.shape
     groups, k = b.shape[0], b.shape[2]
     dev = dd.device
     _check16(b, "b", (groups, n, k), dt, dev)
     _offsets(group_offsets, groups, dev)
-    with _launch_on(dd, stream) as s:
-        da = torch.empty((m, k), dtype=dt, device=dev) if da is None else da
-        _check16(da, "da", (m, k), dt, dev)
+    s, contexts = _begin(dd, stream)
+    try:
+        if da is None:
+            da = dd.new_empty((m, k))
+        else:
+            _check16(da, "da", (m, k), dt, dev)
         _raise(_lib.mx_grouped_gemm_ragged_dgrad(_ptr(dd), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
                                                  _ptr(da), _status_on(dev_status, dev), s),
                "mx_grouped_gemm_ragged_dgrad")
+    finally:
+        _end(contexts)
     return da
 
 
@@ -993,7 +1010,8 @@ def mx_grouped_gemm_ragged_wgrad(dd: torch.Tensor, a: torch.Tensor, group_offset
     -> db [E, N, K], the sum over expert e's rows of dd[i]^T a[i] (zeros for an
     expert without rows), in the operands' type or FP32 (``out_dtype``)."""
     dt = _operand16(dd, "dd", 2)
-    _operand16(a, "a", 2)
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a must be a 2-D torch.Tensor")
     m, n = dd.shape
     k = a.shape[1]
     dev = dd.device
@@ -1005,12 +1023,17 @@ def mx_grouped_gemm_ragged_wgrad(dd: torch.Tensor, a: torch.Tensor, group_offset
     out_dtype = (dt if db is None else db.dtype) if out_dtype is None else out_dtype
     if out_dtype not in (dt, torch.float32):
         raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
-    with _launch_on(dd, stream) as s:
-        db = torch.empty((groups, n, k), dtype=out_dtype, device=dev) if db is None else db
-        _check16(db, "db", (groups, n, k), out_dtype, dev)
+    s, contexts = _begin(dd, stream)
+    try:
+        if db is None:
+            db = dd.new_empty((groups, n, k), dtype=out_dtype)
+        else:
+            _check16(db, "db", (groups, n, k), out_dtype, dev)
         _raise(_lib.mx_grouped_gemm_ragged_wgrad(_ptr(dd), _ptr(a), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
                                                  _DTYPES[out_dtype], _ptr(db), _status_on(dev_status, dev), s),
                "mx_grouped_gemm_ragged_wgrad")
+    finally:
+        _end(contexts)
     return db
 
 
@@ -1049,14 +1072,21 @@ def mx_orthogonalize(g: torch.Tensor, steps: int = 5, coeffs=(3.4445, -4.7750, 2
     m, n = g.shape[-2], g.shape[-1]
     dev = g.device
     need = mx_orthogonalize_workspace_bytes(batch, m, n, g.dtype, steps)
-    with _launch_on(g, stream) as s:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev) if out is None else out
-        _check16(out, "out", g.shape, torch.bfloat16, dev)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    s, contexts = _begin(g, stream)
+    try:
+        if out is None:
+            out = g.new_empty(g.shape, dtype=torch.bfloat16)
+        else:
+            _check16(out, "out", g.shape, torch.bfloat16, dev)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
         _raise(_lib.mx_orthogonalize(_ptr(g), _DTYPES[g.dtype], _ptr(out), batch, m, n, steps,
                                      (ctypes.c_float * len(flat))(*flat), eps, _ptr(workspace), workspace.numel(),
                                      _status_on(dev_status, dev), s), "mx_orthogonalize")
+    finally:
+        _end(contexts)
     return out
 
 

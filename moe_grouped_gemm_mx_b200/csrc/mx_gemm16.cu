@@ -1038,8 +1038,9 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   small kernel: 4 us, the exchange of partial sums, and per K chunk of a CTA
 //     0.25 us where it has an SM to itself (six stages), 0.39 us with three stages,
 //     0.51 us where two share one; the first six chunks 0.15 us more each, and
-//     2.5 us for every further round (64x2112x7168 by 4: 12.9 estimated, 12.9
-//     measured; by 2: 19.5, 19.7; 1037x7168x2048 whole: 42, 38.7).
+//     2.5 us for every further round, and its epilogue, shared by a split
+//     (64x2112x7168 by 4: 13.2 estimated, 12.9 measured; by 2: 20, 19.7;
+//     1037x7168x2048 whole: 43, 38.7).
 struct G16Tiles {
   double pair, small;  // 256 x 256 and 128 x 128 tiles to do
   int64_t chunks;      // of 64 of K
@@ -1067,9 +1068,13 @@ static double pair_cost(const G16Tiles& c, int num_sms) {
   return 8.0 + 0.3 * std::ceil(c.pair / (num_sms / 2)) * static_cast<double>(c.chunks);
 }
 
+// The small kernel's epilogue on a whole tile, in us: C, the mirrored tile and a low
+// half make it longest.
+static double epilogue_cost(const Gemm16& p) { return p.epi == kEpiPoly ? 1.6 : p.epi == kEpiLinear ? 1.0 : 0.5; }
+
 // The small kernel's cost on `tiles` tiles, the longest of `chunks`, and the best
 // split, at most one CTA per chunk of the product with the fewest.
-static double small_cost(double tiles, int64_t chunks, int64_t fewest, int num_sms, int* splits) {
+static double small_cost(double tiles, int64_t chunks, int64_t fewest, double epilogue, int num_sms, int* splits) {
   double best = 1e30;
   *splits = 1;
   for (int s = 1; s <= 8; s *= 2) {
@@ -1077,7 +1082,7 @@ static double small_cost(double tiles, int64_t chunks, int64_t fewest, int num_s
     const double each = static_cast<double>(ceil_div(chunks, s));
     const double exchange = s == 1 ? 0.0 : s == 2 ? 0.6 : s == 4 ? 1.0 : 1.3 + 0.2 * tiles;
     const double rounds = std::ceil(tiles * s / (2.0 * num_sms));
-    double cost = 4.0 + exchange + 0.15 * std::fmin(each, 6.0);
+    double cost = 4.0 + exchange + 0.15 * std::fmin(each, 6.0) + epilogue / s;
     if (tiles <= static_cast<double>(lone_clusters(s, num_sms)))
       cost += 0.25 * each;
     else
@@ -1115,7 +1120,7 @@ static G16Choice choose(const Gemm16& p, int num_sms) {
   }
   if (!small_can(p)) return c;
   const G16Tiles tiles = count_tiles(p);
-  c.small = small_cost(tiles.small, tiles.chunks, tiles.chunks, num_sms, &c.splits) < pair_cost(tiles, num_sms);
+  c.small = small_cost(tiles.small, tiles.chunks, tiles.chunks, epilogue_cost(p), num_sms, &c.splits) < pair_cost(tiles, num_sms);
   return c;
 }
 
@@ -1203,12 +1208,12 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
 cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cudaStream_t stream) {
   const G16Tiles tp = count_tiles(p), tq = count_tiles(q);
   int sp = 1, sq = 1, s = 1;
-  const double apart = std::fmin(small_cost(tp.small, tp.chunks, tp.chunks, num_sms, &sp), pair_cost(tp, num_sms)) +
-                       std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, num_sms, &sq), pair_cost(tq, num_sms));
+  const double apart = std::fmin(small_cost(tp.small, tp.chunks, tp.chunks, epilogue_cost(p), num_sms, &sp), pair_cost(tp, num_sms)) +
+                       std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, epilogue_cost(q), num_sms, &sq), pair_cost(tq, num_sms));
   const int64_t longest = tp.chunks > tq.chunks ? tp.chunks : tq.chunks, fewest = tp.chunks < tq.chunks ? tp.chunks : tq.chunks;
   const bool together = p.mode == kBatched && q.mode == kBatched && p.epi == kEpiPlain && q.epi == kEpiPlain && small_can(p) &&
                         small_can(q) && std::getenv("MX_GEMM16_CONFIG") == nullptr &&
-                        small_cost(tp.small + tq.small, longest, fewest, num_sms, &s) < apart;
+                        small_cost(tp.small + tq.small, longest, fewest, epilogue_cost(p), num_sms, &s) < apart;
   if (!together) {
     const cudaError_t e = launch_gemm16(p, num_sms, stream);
     return e != cudaSuccess ? e : launch_gemm16(q, num_sms, stream);
