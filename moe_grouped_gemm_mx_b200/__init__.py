@@ -897,7 +897,7 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
     dx is None without ``w`` and dw without ``x`` (a frozen layer, or one whose
     input needs no gradient), dbias is None unless ``bias_grad`` or an output
     ``dbias``.  The residual's gradient is dy.  ``dz`` [M, N] receives
-    dy * act'(z)."""
+    dy * act'(z) (with an activation)."""
     dt = _operand16(dy, "dy", 2)
     act = _activation(activation)
     m, n = dy.shape
@@ -912,6 +912,8 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
     k = x.shape[1] if x is not None else w.shape[1]
     if act != 0 and z is None:
         raise ValueError(f"activation {activation!r} needs z")
+    if act == 0 and dz is not None:
+        raise ValueError("without an activation dz is dy itself: it is not written")
     for t, nm, shape in ((x, "x", (m, k)), (w, "w", (n, k)), (z, "z", (m, n))):
         if t is not None:
             _check16(t, nm, shape, dt, dev)

@@ -1037,7 +1037,8 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     measured; 1037x7168x2048 27.2, 28.4; 64x2112x7168 42, 38.5).
 //   small kernel: 4 us, the exchange of partial sums, and per K chunk of a CTA
 //     0.25 us where it has an SM to itself (six stages), 0.39 us with three stages,
-//     0.51 us where two share one; the first six chunks 0.15 us more each, and
+//     0.51 us where two share one (and 1.5 us to start); the first six chunks
+//     0.15 us more each, and
 //     2.5 us for every further round, and its epilogue, shared by a split
 //     (64x2112x7168 by 4: 13.2 estimated, 12.9 measured; by 2: 20, 19.7;
 //     1037x7168x2048 whole: 43, 38.7).
@@ -1086,7 +1087,7 @@ static double small_cost(double tiles, int64_t chunks, int64_t fewest, double ep
     if (tiles <= static_cast<double>(lone_clusters(s, num_sms)))
       cost += 0.25 * each;
     else
-      cost += (tiles * s <= num_sms ? 0.39 : 0.51) * each * rounds + 2.5 * (rounds - 1.0);
+      cost += (tiles * s <= num_sms ? 0.39 * each : 1.5 + 0.51 * each * rounds) + 2.5 * (rounds - 1.0);
     if (cost < best) {
       best = cost;
       *splits = s;
@@ -1104,19 +1105,24 @@ struct G16Choice {
   int splits;
 };
 
+// MX_GEMM16_CONFIG forces a kernel for tests and tuning: 0 the pair kernel, 1, 2, 4
+// or 8 the small one with that many CTAs (at most one per K chunk) a tile.  -1: not set.
+static int forced_config() {
+  const char* v = std::getenv("MX_GEMM16_CONFIG");
+  if (v == nullptr || v[0] == 0 || v[1] != 0) return -1;
+  const int n = v[0] - '0';
+  return n == 0 || n == 1 || n == 2 || n == 4 || n == 8 ? n : -1;
+}
+
 static G16Choice choose(const Gemm16& p, int num_sms) {
   G16Choice c = {false, 1};
-  // MX_GEMM16_CONFIG forces a kernel for tests and tuning: 0 the pair kernel, 1,
-  // 2, 4 or 8 the small one with that many CTAs (at most one per K chunk) a tile
-  if (const char* forced = std::getenv("MX_GEMM16_CONFIG")) {
-    const int v = std::atoi(forced);
-    if (v == 0 || !small_can(p)) return c;
-    if (v == 1 || v == 2 || v == 4 || v == 8) {
-      c.small = true;
-      for (c.splits = v; c.splits > ceil_div(p.k, kS16K); c.splits /= 2) {
-      }
-      return c;
+  const int forced = forced_config();
+  if (forced >= 0) {
+    if (forced == 0 || !small_can(p)) return c;
+    c.small = true;
+    for (c.splits = forced; c.splits > ceil_div(p.k, kS16K); c.splits /= 2) {
     }
+    return c;
   }
   if (!small_can(p)) return c;
   const G16Tiles tiles = count_tiles(p);
@@ -1212,7 +1218,7 @@ cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cud
                        std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, epilogue_cost(q), num_sms, &sq), pair_cost(tq, num_sms));
   const int64_t longest = tp.chunks > tq.chunks ? tp.chunks : tq.chunks, fewest = tp.chunks < tq.chunks ? tp.chunks : tq.chunks;
   const bool together = p.mode == kBatched && q.mode == kBatched && p.epi == kEpiPlain && q.epi == kEpiPlain && small_can(p) &&
-                        small_can(q) && std::getenv("MX_GEMM16_CONFIG") == nullptr &&
+                        small_can(q) && forced_config() < 0 &&
                         small_cost(tp.small + tq.small, longest, fewest, epilogue_cost(p), num_sms, &s) < apart;
   if (!together) {
     const cudaError_t e = launch_gemm16(p, num_sms, stream);

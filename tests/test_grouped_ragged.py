@@ -273,6 +273,42 @@ def test_expert_layer_step(mx):
         assert bool((got[:large] > 0.5).all()) and bool((got < 1.3).all())
 
 
+def test_more_elements_than_32_bits_count(mx):
+    """Weights, their gradients and the grouped rows each of more than 2^31 elements."""
+    groups, n, k = 66, 8192, 4096                       # 2.2e9 weights
+    counts = [3] * groups
+    counts[5] = 0
+    off = offsets_of(counts)
+    m = sum(counts)
+    a, dd = normal((m, k), BF16, 1), normal((m, n), BF16, 2)
+    b = torch.empty((groups, n, k), dtype=BF16, device="cuda").fill_(0.25)
+    b[-1] = normal((n, k), BF16, 3, 0.02)
+    d = mx.mx_grouped_gemm_ragged(a, b, off)
+    da = mx.mx_grouped_gemm_ragged_dgrad(dd, b, off)
+    for e in (0, 5, groups - 1):
+        s = slice(int(off[e]), int(off[e + 1]))
+        be = b[e].double()
+        ref = a[s].double() @ be.T
+        close(d[s], ref, product_tol(ref, a[s].double().abs() @ be.abs().T, k, BF16), f"d of expert {e}")
+        ref = dd[s].double() @ be
+        close(da[s], ref, product_tol(ref, dd[s].double().abs() @ be.abs(), n, BF16), f"da of expert {e}")
+    del b, d, da
+    db = mx.mx_grouped_gemm_ragged_wgrad(dd, a, off)
+    for e in (0, 5, groups - 1):
+        s = slice(int(off[e]), int(off[e + 1]))
+        ref = dd[s].double().T @ a[s].double()
+        close(db[e], ref, product_tol(ref, dd[s].double().abs().T @ a[s].double().abs(), 3, BF16), f"db of expert {e}")
+    del db
+    m = 600 * 1024                                      # 2.5e9 results in two experts
+    off = offsets_of([m // 2 + 77, m - m // 2 - 77])
+    a, b = normal((m, 64), BF16, 4), normal((2, 4096, 64), BF16, 5, 0.125)
+    d = mx.mx_grouped_gemm_ragged(a, b, off)
+    for row in (0, int(off[1]) - 1, int(off[1]), 524287, 524288, m - 1):
+        e = int(row >= int(off[1]))
+        ref = a[row].double() @ b[e].double().T
+        close(d[row], ref, product_tol(ref, a[row].double().abs() @ b[e].double().abs().T, 64, BF16), f"row {row}")
+
+
 def test_python_refusals(mx):
     a, b = normal((16, 64), BF16, 1), normal((2, 32, 64), BF16, 2)
     off = offsets_of([7, 9])

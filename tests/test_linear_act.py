@@ -331,6 +331,41 @@ def test_wait_timeout_reported(mx):
             close(y, ref, product_tol(ref, x.double().abs() @ w.double().abs().T, x.shape[1], BF16), "after the timeout")
 
 
+def test_more_elements_than_32_bits_count(mx):
+    """An output of 2.4e9 elements: rows behind the 2^31st element are right, in the
+    forward pass and in dz (the residual, the pre-activation and the bias sums cross it too)."""
+    m, n, k = 600 * 1024 + 8, 4096, 64
+    x, w, b = normal((m, k), BF16, 1), normal((n, k), BF16, 2, 0.125), normal((n,), BF16, 3)
+    r = torch.empty((m, n), dtype=BF16, device="cuda").fill_(0.5)
+    y, z = mx.mx_linear_act(x, w, bias=b, residual=r, activation="relu", return_z=True)
+    rows = torch.tensor([0, 1, 524286, 524287, 524288, 524289, m - 130, m - 1], device="cuda")
+    ry, dy, rz, dz = forward_ref(x[rows], w, b, r[rows], "relu")
+    close(y[rows], ry, U[BF16] * ry.abs() + 1.01 * dy, "y")
+    close(z[rows], rz, U[BF16] * rz.abs() + 1.01 * dz, "z")
+    del r
+    g = y                      # any gradient: the outputs themselves
+    dzt = torch.empty_like(z)
+    dx, dw, db = mx.mx_linear_act_backward(g, x, w, z=z, activation="relu", bias_grad=True, dz=dzt)
+    assert torch.equal(dzt[rows], torch.where(z[rows] > 0, g[rows], torch.zeros_like(g[rows])))
+    ref = dzt[rows].double() @ w.double()
+    close(dx[rows], ref, product_tol(ref, dzt[rows].double().abs() @ w.double().abs(), n, BF16), "dx")
+    cols = torch.tensor([0, 7, 2048, 4095], device="cuda")
+    sub = dzt[:, cols].double()
+    ref = sub.T @ x.double()
+    close(dw[cols], ref, product_tol(ref, sub.abs().T @ x.double().abs(), m, BF16), "dw")
+    ref = sub.sum(0)
+    close(db[cols], ref, U[BF16] * ref.abs() + (m + 64) * 2.0 ** -24 * sub.abs().sum(0), "dbias")
+
+
+def test_empty_setting_is_no_setting(mx, monkeypatch):
+    x, w = normal((70, 520), BF16, 1), normal((264, 520), BF16, 2, 0.05)
+    want = mx.mx_linear_act(x, w)
+    monkeypatch.setenv("MX_GEMM16_CONFIG", "")
+    assert torch.equal(mx.mx_linear_act(x, w), want)
+    monkeypatch.setenv("MX_GEMM16_CONFIG", "no")
+    assert torch.equal(mx.mx_linear_act(x, w), want)
+
+
 def test_python_refusals(mx):
     x, w = normal((16, 64), BF16, 1), normal((32, 64), BF16, 2)
     with pytest.raises(TypeError):
@@ -347,6 +382,8 @@ def test_python_refusals(mx):
         mx.mx_linear_act(x, w, bias=torch.zeros(31, dtype=BF16, device="cuda"))
     with pytest.raises(ValueError):
         mx.mx_linear_act(x.cpu(), w)
+    with pytest.raises(ValueError):                                                 # dz without an activation
+        mx.mx_linear_act_backward(normal((16, 32), BF16, 3), x, w, dz=normal((16, 32), BF16, 3))
     with pytest.raises(mx.MXError):
         mx.mx_linear_act(normal((16, 60), BF16, 1), normal((32, 60), BF16, 2))      # k % 8
     with pytest.raises(mx.MXError):

@@ -242,6 +242,17 @@ def test_captured_and_two_streams(mx):
     assert all(torch.equal(r, w) for runs, w in zip(got, want) for r in runs)
 
 
+def test_more_elements_than_32_bits_count(mx):
+    """A batch of 2.2e9 elements: its last matrices are right."""
+    batch, m, n = 66, 4096, 8192
+    g = torch.empty((batch, m, n), dtype=BF16, device="cuda").fill_(1e-3)
+    g[0] = momentum(1, m, n, BF16, seed=31)[0]
+    g[-1] = momentum(1, m, n, BF16, seed=32)[0]
+    got = mx.mx_orthogonalize(g, steps=2)
+    for i in (0, batch - 1):
+        check(g[i], got[i], [COEFFS] * 2, what=f"matrix {i}")
+
+
 def test_empty(mx):
     for shape in ((0, 8, 8), (2, 0, 8), (2, 8, 0)):
         assert mx.mx_orthogonalize(torch.empty(shape, dtype=BF16, device="cuda")).shape == shape
