@@ -871,9 +871,9 @@ def mx_linear_act(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = 
     s, contexts = _begin(x, stream)
     try:
         if y is None:
-            y = x.new_empty((m, n))
+            y = x.new_empty(m, n)
         if return_z and z is None:
-            z = x.new_empty((m, n))
+            z = x.new_empty(m, n)
         _raise(_lib.mx_linear_act(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(z), _ptr(y), m, n, k, _DTYPES[dt],
                                   act, _status_on(dev_status, dev), s), "mx_linear_act")
     finally:
@@ -910,28 +910,37 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
         if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 2):
             raise ValueError(f"{nm} must be a 2-D torch.Tensor")
     k = x.shape[1] if x is not None else w.shape[1]
-    if act != 0 and z is None:
+    if act == 0:
+        if dz is not None:
+            raise ValueError("without an activation dz is dy itself: it is not written")
+    elif z is None:
         raise ValueError(f"activation {activation!r} needs z")
-    if act == 0 and dz is not None:
-        raise ValueError("without an activation dz is dy itself: it is not written")
-    for t, nm, shape in ((x, "x", (m, k)), (w, "w", (n, k)), (z, "z", (m, n))):
-        if t is not None:
-            _check16(t, nm, shape, dt, dev)
-    for t, nm, shape in ((dx, "dx", (m, k)), (dw, "dw", (n, k)), (dbias, "dbias", (n,)), (dz, "dz", (m, n))):
-        if t is not None:
-            _check16(t, nm, shape, dt, dev)
+    if x is not None:
+        _check16(x, "x", (m, k), dt, dev)
+    if w is not None:
+        _check16(w, "w", (n, k), dt, dev)
+    if z is not None:
+        _check16(z, "z", (m, n), dt, dev)
+    if dx is not None:
+        _check16(dx, "dx", (m, k), dt, dev)
+    if dw is not None:
+        _check16(dw, "dw", (n, k), dt, dev)
+    if dbias is not None:
+        _check16(dbias, "dbias", (n,), dt, dev)
+    if dz is not None:
+        _check16(dz, "dz", (m, n), dt, dev)
     if workspace is not None:
         _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
     s, contexts = _begin(dy, stream)
     try:
         if w is not None and dx is None:
-            dx = dy.new_empty((m, k))
+            dx = dy.new_empty(m, k) if x is None else torch.empty_like(x)
         if x is not None and dw is None:
-            dw = dy.new_empty((n, k))
+            dw = dy.new_empty(n, k) if w is None else torch.empty_like(w)
         if bias_grad and dbias is None:
             dbias = dy.new_empty(n)
         if act != 0 and dz is None:
-            dz = dy.new_empty((m, n))
+            dz = torch.empty_like(dy)
         if dbias is not None and workspace is None and m > 0 and n > 0:
             need = mx_linear_act_backward_workspace_bytes(m, n)
             if need:
@@ -967,7 +976,7 @@ def mx_grouped_gemm_ragged(a: torch.Tensor, b: torch.Tensor, group_offsets: torc
     s, contexts = _begin(a, stream)
     try:
         if d is None:
-            d = a.new_empty((m, n))
+            d = a.new_empty(m, n)
         else:
             _check16(d, "d", (m, n), dt, dev)
         _raise(_lib.mx_grouped_gemm_ragged(_ptr(a), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt], _ptr(d),
@@ -994,7 +1003,7 @@ def mx_grouped_gemm_ragged_dgrad(dd: torch.Tensor, b: torch.Tensor, group_offset
     s, contexts = _begin(dd, stream)
     try:
         if da is None:
-            da = dd.new_empty((m, k))
+            da = dd.new_empty(m, k)
         else:
             _check16(da, "da", (m, k), dt, dev)
         _raise(_lib.mx_grouped_gemm_ragged_dgrad(_ptr(dd), _ptr(b), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
@@ -1028,7 +1037,7 @@ def mx_grouped_gemm_ragged_wgrad(dd: torch.Tensor, a: torch.Tensor, group_offset
     s, contexts = _begin(dd, stream)
     try:
         if db is None:
-            db = dd.new_empty((groups, n, k), dtype=out_dtype)
+            db = dd.new_empty(groups, n, k, dtype=out_dtype)
         else:
             _check16(db, "db", (groups, n, k), out_dtype, dev)
         _raise(_lib.mx_grouped_gemm_ragged_wgrad(_ptr(dd), _ptr(a), _ptr(group_offsets), groups, m, n, k, _DTYPES[dt],
