@@ -689,6 +689,7 @@ mx_status mx_linear_act(const void* x, const void* w, const void* bias, const vo
   g.bias = bias;
   g.res = residual;
   g.res_ld = n;
+  g.res_batch = m * n;
   g.z = z;
   g.act = act;
   return from_cuda(mxk::launch_gemm16(g, sms, static_cast<cudaStream_t>(stream)));

@@ -10,7 +10,7 @@
 //      warp 0      TMA producer (both CTAs): 64 elements of K per stage
 //      warp 1      MMA issuer (leader), K = 16 per instruction
 //      warps 2-9   epilogue: two warps per TMEM lane quarter, 128 columns each
-//                  (linear: warps 2-17, four per quarter, 64 columns each)
+//                  (linear and poly: warps 2-17, four per quarter, 64 columns each)
 //      warp 10     ragged K only (both CTAs): clears the rows of the stage that
 //                  lie behind the group's last token before the MMAs read them
 //
@@ -32,21 +32,23 @@ namespace mxk {
 
 // ======================================================================= CTA-pair kernel
 
-// Epilogue warps: the linear epilogue's arithmetic (an activation is some 20
-// instructions a value) wants four to a scheduler; the others keep 8 with more
-// registers.  One more warp clears rows (ragged K; never with the linear epilogue).
-__host__ __device__ constexpr int p16_epi_warps(int epi) { return epi == kEpiLinear ? 16 : 8; }
-__host__ __device__ constexpr int p16_threads(int epi) { return 32 * (2 + p16_epi_warps(epi) + (epi == kEpiLinear ? 0 : 1)); }
+// Epilogue warps: the arithmetic of the linear and poly epilogues (an activation is
+// some 20 instructions a value) wants four to a scheduler; plain and sum keep 8 with
+// more registers.  One more warp clears rows (ragged K, plain and sum only).
+__host__ __device__ constexpr int p16_epi_warps(int epi) { return epi == kEpiLinear || epi == kEpiPoly ? 16 : 8; }
+__host__ __device__ constexpr int p16_threads(int epi) {
+  return 32 * (2 + p16_epi_warps(epi) + (p16_epi_warps(epi) == 16 ? 0 : 1));
+}
 constexpr int kP16TM = 256, kP16TN = 256;
 constexpr int kP16K = 64;     // elements of K per stage
 constexpr int kP16Seg = 512;  // kEpiSum: K per partial sum
 
-// The linear epilogue's 16 warps take a stage's place for their staging tiles,
-// where the residual's rows wait for the sum (five stages cost about 1 % of a long
+// 16 epilogue warps take a stage's place for their staging tiles, where the
+// residual's (or C's) rows wait for the sum (five stages cost about 1 % of a long
 // product).
 template <int EPI>
 struct P16Layout {
-  static constexpr int STAGES = EPI == kEpiLinear ? 5 : 6;
+  static constexpr int STAGES = p16_epi_warps(EPI) == 16 ? 5 : 6;
   static constexpr int WARPS = p16_epi_warps(EPI);
   static constexpr int OP_BYTES = 128 * 128;        // 16 KB: one operand's half tile of a stage
   static constexpr int OFF_A = 0;
@@ -404,116 +406,15 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
             if (col_w + c * 32 < args.n)
               put(&tmap_d, reinterpret_cast<const uint32_t*>(sum) + c * 32, col_w + c * 32, row_w, z_out);
         }
-      } else if constexpr (EPI == kEpiLinear) {
-        // 64 columns a warp, 32 at a time; a pre-activation that is wanted takes a pass
-        // of its own over the accumulator, so that one staging tile does.  The
-        // residual's rows come into the tile by TMA, while the MMAs run if they can, and
-        // the result takes their place.
-        const bool has_res = args.res != nullptr && mine;
-        auto fetch_res = [&]() {
-          if (lane == 0) {
-            bulk_wait_group_read<0>();
-            mbar_arrive_expect_tx(res_bar(ew), L::STG_BYTES);
-            tma_load_3d(stg, &tmap_r, res_bar(ew), col_w, row_w, 0);
-          }
-        };
-        auto load32 = [&](int c, float (&v)[32]) {  // accumulator and bias
-          uint32_t raw[32];
-          tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
-          if (args.bias != nullptr) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (col_w + c + q * 8 < args.n) {
-                float b[8];
-                load8(static_cast<const uint16_t*>(args.bias) + col_w + c + q * 8, args.op_fp16, b);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[q * 8 + j] += b[j];
-              }
-            }
-          }
-        };
-        auto stage32 = [&](int c, const float (&v)[32]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t at = stg + lane * 128 + (((c / 8 + j) ^ (lane & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack16(v[8 * j], v[8 * j + 1], h)),
-                         "r"(pack16(v[8 * j + 2], v[8 * j + 3], h)), "r"(pack16(v[8 * j + 4], v[8 * j + 5], h)),
-                         "r"(pack16(v[8 * j + 6], v[8 * j + 7], h))
-                         : "memory");
-          }
-        };
-        if (has_res && args.z == nullptr) fetch_res();
+      } else if constexpr (EPI == kEpiPlain) {
         ok = wait_full();
         if (!ok) break;
-        if (mine && args.z != nullptr) {
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-#pragma unroll 1
-          for (int c = 0; c < 64; c += 32) {
-            float v[32];
-            load32(c, v);
-            stage32(c, v);
-          }
-          send(&tmap_z, col_w, row_w, 0);
-          if (has_res) fetch_res();
-        }
-        if (has_res) {
-          ok = wait16<false>(res_bar(ew), res_phase, abort_flag, args.wait_ns);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) {
-            if (lane == 0) {
-              report(args.status, 0x4);
-              *abort_flag = 1;
-            }
-            break;
-          }
-          res_phase ^= 1u;
-        } else {
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          if (mine) {
-            float v[32];
-            load32(c, v);
-            uint4 res[4];
-            if (has_res) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const uint32_t from = stg + lane * 128 + (((c / 8 + q) ^ (lane & 7)) << 4);
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(res[q].x), "=r"(res[q].y), "=r"(res[q].z), "=r"(res[q].w)
-                             : "r"(from)
-                             : "memory");
-              }
-            }
-            if (c == 32) release();
-            g16_activate<32>(args, v, res);
-            stage32(c, v);
-          } else if (c == 32) {
-            release();
-          }
-        }
-        if (mine) send(&tmap_d, col_w, row_w, 0);
-      } else {
-        ok = wait_full();
-        if (!ok) break;
-        const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
           const int col0 = col_w + c;
           if (!mine || col0 >= args.n) {
             if (c == 64) release();
             continue;
-          }
-          uint4 res[8], low[8];
-          if constexpr (EPI == kEpiPoly) {
-            g16_load_res<64>(args, args.res, tl.group, row, col0, args.n, valid, res);
-            g16_load_res<64>(args, args.res_lo, tl.group, row, col0, args.n, valid, low);
           }
           float v[64];
           {
@@ -525,24 +426,163 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
             for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(raw[j / 32][j % 32]);
           }
           if (c == 64) release();
-          auto put64 = [&](const CUtensorMap* map) {
+          if (tma) {
             uint32_t w[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) w[j] = pack16(v[2 * j], v[2 * j + 1], h);
-            put(map, w, col0, row_w, z_out);
-          };
-          g16_epilogue<EPI, 64>(args, v, res, low, nullptr, tl.group, row, col0, scale);
-          if (tma)
-            put64(&tmap_d);
-          else if (valid)
+            put(&tmap_d, w, col0, row_w, z_out);
+          } else if (valid) {
             g16_store_row<64>(args, args.d, v, tl.group, row, col0, args.n);
-          if constexpr (EPI == kEpiPoly) {
-            if (args.sym && tl.mb != tl.nb && valid) g16_store_mirror<64>(args, v, tl.group, row, col0, args.n);
-            if (args.z != nullptr) {
-              g16_remainder<64>(args, v);
-              put64(&tmap_z);
+          }
+        }
+      } else {
+        // 64 columns a warp, 32 at a time.  The rows of the residual or C come into the
+        // staging tile by TMA, while the MMAs run if they can, and the result takes
+        // their place.
+        const bool has_res = args.res != nullptr && mine;
+        auto tile_free = [&]() {  // the last store has read the staging tile
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        };
+        auto fetch_res = [&]() {
+          if (lane == 0) {
+            bulk_wait_group_read<0>();
+            mbar_arrive_expect_tx(res_bar(ew), L::STG_BYTES);
+            tma_load_3d(stg, &tmap_r, res_bar(ew), col_w, row_w, tl.group);
+          }
+        };
+        auto wait_res = [&]() -> bool {
+          const bool got = wait16<false>(res_bar(ew), res_phase, abort_flag, args.wait_ns);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            if (lane == 0) {
+              report(args.status, 0x4);
+              *abort_flag = 1;
+            }
+            return false;
+          }
+          res_phase ^= 1u;
+          return true;
+        };
+        // 32 columns from `c` of the warp's 64: the accumulator, and this lane's row of the tile
+        auto acc32 = [&](int c, float (&v)[32]) {
+          uint32_t raw[32];
+          tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+        };
+        auto at8 = [&](int c) { return stg + lane * 128 + (((c / 8) ^ (lane & 7)) << 4); };
+        auto staged32 = [&](int c, uint4 (&w)[4]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[q].x), "=r"(w[q].y), "=r"(w[q].z), "=r"(w[q].w)
+                         : "r"(at8(c + q * 8))
+                         : "memory");
+        };
+        auto stage32 = [&](int c, const uint4 (&w)[4]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at8(c + q * 8)), "r"(w[q].x), "r"(w[q].y),
+                         "r"(w[q].z), "r"(w[q].w)
+                         : "memory");
+        };
+        auto pack32 = [&](const float (&v)[32], uint4 (&w)[4]) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = make_uint4(pack16(v[8 * q], v[8 * q + 1], h), pack16(v[8 * q + 2], v[8 * q + 3], h),
+                              pack16(v[8 * q + 4], v[8 * q + 5], h), pack16(v[8 * q + 6], v[8 * q + 7], h));
+        };
+        if constexpr (EPI == kEpiLinear) {
+          auto pre32 = [&](int c, float (&v)[32]) {  // the pre-activation
+            acc32(c, v);
+            if (args.bias != nullptr) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (col_w + c + q * 8 < args.n) {
+                  float b[8];
+                  load8(static_cast<const uint16_t*>(args.bias) + col_w + c + q * 8, args.op_fp16, b);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[q * 8 + j] += b[j];
+                }
+              }
+            }
+          };
+          if (has_res && args.z == nullptr) fetch_res();
+          ok = wait_full();
+          if (!ok) break;
+          if (mine && args.z != nullptr) {
+            // a pre-activation that is wanted takes a pass of its own over the
+            // accumulator, so that one staging tile does
+            tile_free();
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              float v[32];
+              uint4 w[4];
+              pre32(c, v);
+              pack32(v, w);
+              stage32(c, w);
+            }
+            send(&tmap_z, col_w, row_w, 0);
+            if (has_res) fetch_res();
+          }
+          if (has_res) {
+            ok = wait_res();
+            if (!ok) break;
+          } else {
+            tile_free();
+          }
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            if (mine) {
+              float v[32];
+              uint4 w[4];
+              pre32(c, v);
+              if (c == 32) release();
+              if (has_res) staged32(c, w);
+              g16_activate<32>(args, v, w);
+              pack32(v, w);
+              stage32(c, w);
+            } else if (c == 32) {
+              release();
             }
           }
+          if (mine) send(&tmap_d, col_w, row_w, 0);
+        } else {
+          if (has_res) fetch_res();
+          ok = wait_full();
+          if (!ok) break;
+          if (has_res) {
+            ok = wait_res();
+            if (!ok) break;
+          } else {
+            tile_free();
+          }
+          const float scale = g16_scale(args, tl.group);
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            if (mine) {
+              uint4 res[4], low[4];
+              g16_load_res<32>(args, args.res_lo, tl.group, row, col_w + c, args.n, valid, low);
+              float v[32];
+              acc32(c, v);
+              if (c == 32) release();
+              if (has_res) staged32(c, res);
+              g16_epilogue<EPI, 32>(args, v, res, low, nullptr, tl.group, row, col_w + c, scale);
+              if (args.sym && tl.mb != tl.nb)
+                g16_store_mirror<32>(args, v, tl.group, row, col_w + c, args.n, valid);
+              uint4 w[4];
+              pack32(v, w);
+              stage32(c, w);
+              if (args.z != nullptr && valid) {  // the low half of D, past the staging tile
+                g16_remainder<32>(args, v);
+                g16_store_row<32>(args, args.z, v, tl.group, row, col_w + c, args.n);
+              }
+            } else if (c == 32) {
+              release();
+            }
+          }
+          if (mine) send(&tmap_d, col_w, row_w, tl.group);
         }
       }
     }
@@ -834,10 +874,12 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
           if (args.z != nullptr && valid) g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
           g16_activate<32>(args, v, res[ci]);
         }
+        if constexpr (EPI == kEpiPoly) {
+          if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, col_end, valid);
+        }
         if (valid) {
           g16_store_row<32>(args, args.d, v, tl.group, row, col0, col_end);
           if constexpr (EPI == kEpiPoly) {
-            if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, col_end);
             if (args.z != nullptr) {
               g16_remainder<32>(args, v);
               g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
@@ -1198,10 +1240,9 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
   }
   const int64_t d_depth = p.mode == kRaggedM ? 1 : p.groups;
   if (!make_tmap_out16(&td, p.d, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2)) return cudaErrorInvalidValue;
-  if (p.z && !make_tmap_out16(&tz, p.z, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2))
+  if (p.z && p.epi == kEpiLinear && !make_tmap_out16(&tz, p.z, p.n, p.m, d_depth, p.d_ld, p.d_batch, p.out_type == 2))
     return cudaErrorInvalidValue;
-  if (p.epi == kEpiLinear && p.res &&
-      !make_tmap_out16(&tr, const_cast<void*>(p.res), p.n, p.m, 1, p.res_ld, p.m * p.res_ld, false))
+  if (p.res && !make_tmap_out16(&tr, const_cast<void*>(p.res), p.n, p.m, p.groups, p.res_ld, p.res_batch, false))
     return cudaErrorInvalidValue;
   if (p.out_type == 2) return launch_pair16<kEpiSum>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);

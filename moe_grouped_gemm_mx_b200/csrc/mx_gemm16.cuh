@@ -495,16 +495,24 @@ __device__ __forceinline__ void g16_store_row(const G16Args& a, void* out, const
 }
 
 // The mirrored half of a symmetric D (16-bit): column col0 + j of this row
-// becomes row col0 + j; a warp's 32 rows are 64 consecutive bytes there.
+// becomes row col0 + j.  Neighbouring lanes trade values, so that each stores two
+// rows of one column of a pair: a warp's 32 rows are 64 consecutive bytes there.
+// Every lane of the warp calls.  The pair of an odd last row reaches into the row's
+// padding (rows are padded to a multiple of 8 elements).
 template <int C>
 __device__ __forceinline__ void g16_store_mirror(const G16Args& a, const float (&v)[C], int group, int64_t row,
-                                                 int col0, int end) {
-  uint16_t* out = static_cast<uint16_t*>(a.d) + group * a.d_batch + row;
+                                                 int col0, int end, bool valid) {
+  const int odd = threadIdx.x & 1;
+  const bool pair_valid = __shfl_sync(0xFFFFFFFFu, static_cast<int>(valid), threadIdx.x & 30) != 0;
+  uint16_t* out = static_cast<uint16_t*>(a.d) + group * a.d_batch + (row - odd);
 #pragma unroll
   for (int j = 0; j < C; j += 2) {
     const uint32_t w = pack16(v[j], v[j + 1], a.out_type == 1);
-    if (col0 + j < end) out[(col0 + j) * a.d_ld] = static_cast<uint16_t>(w & 0xFFFFu);
-    if (col0 + j + 1 < end) out[(col0 + j + 1) * a.d_ld] = static_cast<uint16_t>(w >> 16);
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+    // an even lane takes column j of rows row and row + 1, an odd one column j + 1 of row - 1 and row
+    const uint32_t two = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+    const int col = col0 + j + odd;
+    if (pair_valid && col < end) *reinterpret_cast<uint32_t*>(out + col * a.d_ld) = two;
   }
 }
 

@@ -101,32 +101,47 @@ __global__ void __launch_bounds__(256) ns_start_kernel(const T* __restrict__ g, 
     }
   }
   __syncthreads();
+  // 2^(sx - e) in two halves: neither leaves FP32's range
   const int e = log_sx - exponent;
+  const float up0 = scalbnf(1.0f, e / 2), up1 = scalbnf(1.0f, e - e / 2);
   const T* x = g + blockIdx.y * m * n;
   __half* xh = hi + blockIdx.y * m * pitch;
   __half* xl = lo == nullptr ? nullptr : lo + blockIdx.y * m * pitch;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + warp; r < m; r += static_cast<int64_t>(gridDim.x) * 8) {
-    if constexpr (sizeof(T) == 2) {
-      if (n % 8 == 0) {
-        for (int c = lane * 8; c < n; c += 256) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + r * n + c));
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[4];
+    if (n % 8 == 0) {
+#pragma unroll 2
+      for (int c = lane * 8; c < n; c += 256) {
+        float f[8];
+        if constexpr (sizeof(T) == 4) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(x + r * n + c)), b = __ldg(reinterpret_cast<const float4*>(x + r * n + c + 4));
+          f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        } else {
+          load8(x + r * n + c, 0, f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] * up0 * up1;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack16(f[2 * j], f[2 * j + 1], 1);
+        *reinterpret_cast<uint4*>(xh + r * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (xl != nullptr) {
+          uint32_t l[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack16(u[j], 0);
-            o[j] = pack16(scalbnf(f.x, e), scalbnf(f.y, e), 1);
+            const float2 back = unpack16(o[j], 1);
+            l[j] = pack16(f[2 * j] - back.x, f[2 * j + 1] - back.y, 1);
           }
-          *reinterpret_cast<uint4*>(xh + r * pitch + c) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(xl + r * pitch + c) = make_uint4(l[0], l[1], l[2], l[3]);
         }
-        continue;
       }
-    }
-    for (int c = lane; c < n; c += 32) {
-      const float v = scalbnf(static_cast<float>(x[r * n + c]), e);
-      const __half h = __float2half_rn(v);
-      xh[r * pitch + c] = h;
-      if (xl != nullptr) xl[r * pitch + c] = __float2half_rn(v - __half2float(h));
+    } else {
+#pragma unroll 4
+      for (int c = lane; c < n; c += 32) {
+        const float v = static_cast<float>(x[r * n + c]) * up0 * up1;
+        const __half h = __float2half_rn(v);
+        xh[r * pitch + c] = h;
+        if (xl != nullptr) xl[r * pitch + c] = __float2half_rn(v - __half2float(h));
+      }
     }
   }
 }
