@@ -471,6 +471,7 @@ mx_status mx_moe_combine_peer(const void *const *y_peers, int32_t ranks, int64_t
  * page, FP8 mixed precision: sensitive parts stay in BF16).  Operands are BF16
  * or FP16, row-major, 16-byte aligned; sums are FP32; results are rounded once.
  * Row lengths that a tensor map must describe are multiples of 8 elements.
+ * Sizes are at most 2^31 - 1024, and what a product sums over at most 2^27.
  */
 typedef enum mx_dtype { MX_BF16 = 0, MX_FP16 = 1, MX_FP32 = 2 } mx_dtype;
 
@@ -491,7 +492,7 @@ typedef enum mx_activation {
  *   `dtype` (MX_BF16 or MX_FP16); y [m, n] out; z [m, n] out (nullable): the
  *   pre-activation, for mx_linear_act_backward.  y is computed from the FP32 z.
  *   y may be the residual itself; outputs overlap nothing else.
- * Requires k > 0, k % 8 == 0, n % 8 == 0, sizes at most 2^31 - 1024.
+ * Requires k > 0, k % 8 == 0, n % 8 == 0.
  * m == 0 or n == 0 is a no-op.
  */
 mx_status mx_linear_act(const void *x, const void *w, const void *bias, const void *residual, void *z, void *y,
@@ -527,7 +528,7 @@ mx_status mx_linear_act_backward(const void *dy, const void *z, const void *x, c
  * (forward, dgrad) and add nothing (wgrad); an expert without rows gets a zero
  * db.  What the rows outside a group hold, infinities and NaN included, does not
  * reach it.  wgrad's result is `dtype` or MX_FP32 (out_dtype).  Requires k and
- * n positive multiples of 8, groups <= 1024, m_total <= 2^31 - 1024.
+ * n positive multiples of 8, groups <= 1024.
  * m_total == 0 is a no-op (wgrad: zeros).  Offsets out of order or range set
  * MX_DEV_BAD_OFFSETS and nothing is written.
  */

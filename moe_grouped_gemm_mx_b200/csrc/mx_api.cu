@@ -619,6 +619,9 @@ mx_status mx_moe_combine_peer(const void* const* y_peers, int32_t ranks, int64_t
 // Row and tile numbers of the 16-bit kernels are 32-bit, with room for a tile
 // behind the last row.
 constexpr int64_t kMaxDim16 = (int64_t(1) << 31) - 1024;
+// What one tile sums over: 2^27 take about a second on a pair of SMs, and a wait
+// for an accumulator may take two (mx_set_wait_limit_ns).
+constexpr int64_t kMaxSum16 = int64_t(1) << 27;
 
 static bool dtype16(int32_t t) { return t == MX_BF16 || t == MX_FP16; }
 
@@ -668,7 +671,7 @@ static mxk::Gemm16 dense16(const void* a, int a_mn, const void* b, int b_mn, voi
 static mx_status check_linear(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t act) {
   if (m < 0 || n < 0 || k < 0 || !dtype16(dtype) || act < MX_ACT_NONE || act > MX_ACT_GELU_TANH)
     return MX_ERR_INVALID_ARGUMENT;
-  if (k == 0 || k % 8 != 0 || n % 8 != 0 || m > kMaxDim16 || n > kMaxDim16 || k > kMaxDim16)
+  if (k == 0 || k % 8 != 0 || n % 8 != 0 || m > kMaxDim16 || n > kMaxDim16 || k > kMaxSum16)
     return MX_ERR_UNSUPPORTED_SHAPE;
   return MX_OK;
 }
@@ -706,6 +709,7 @@ mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, c
                                  void* workspace, size_t workspace_bytes, int32_t* dev_status, mx_stream_t stream) {
   mx_status st = check_linear(m, n, k, dtype, act);
   if (st != MX_OK) return st;
+  if ((dx && n > kMaxSum16) || (dw && m > kMaxSum16)) return MX_ERR_UNSUPPORTED_SHAPE;
   if (misaligned16({dy, z, x, w, dz, dx, dw, dbias, workspace})) return MX_ERR_MISALIGNED;
   if (m == 0 || n == 0) {  // empty sums
     if (m > 0 && dx) return zero_bytes(dx, m * k * 2, stream);
@@ -738,11 +742,12 @@ mx_status mx_linear_act_backward(const void* dy, const void* z, const void* x, c
 }
 
 static mx_status check_ragged(const void* a, const void* b, const int32_t* group_offsets, int32_t groups,
-                              int64_t m_total, int64_t n, int64_t k, int32_t dtype, const void* d, bool* empty) {
+                              int64_t m_total, int64_t n, int64_t k, int64_t summed, int32_t dtype, const void* d,
+                              bool* empty) {
   *empty = false;
   if (groups < 0 || m_total < 0 || n < 0 || k < 0 || !dtype16(dtype)) return MX_ERR_INVALID_ARGUMENT;
   if (n == 0 || k == 0 || n % 8 != 0 || k % 8 != 0 || n > kMaxDim16 || k > kMaxDim16 || m_total > kMaxDim16 ||
-      groups > kMaxGroups)
+      groups > kMaxGroups || summed > kMaxSum16)
     return MX_ERR_UNSUPPORTED_SHAPE;
   if (groups == 0 || m_total == 0) {
     *empty = true;
@@ -757,7 +762,7 @@ mx_status mx_grouped_gemm_ragged(const void* a, const void* b, const int32_t* gr
                                  int64_t m_total, int64_t n, int64_t k, int32_t dtype, void* d, int32_t* dev_status,
                                  mx_stream_t stream) {
   bool empty;
-  mx_status st = check_ragged(a, b, group_offsets, groups, m_total, n, k, dtype, d, &empty);
+  mx_status st = check_ragged(a, b, group_offsets, groups, m_total, n, k, k, dtype, d, &empty);
   if (st != MX_OK || empty) return st;
   int sms;
   int32_t* status;
@@ -774,7 +779,7 @@ mx_status mx_grouped_gemm_ragged_dgrad(const void* dd, const void* b, const int3
                                        int64_t m_total, int64_t n, int64_t k, int32_t dtype, void* da,
                                        int32_t* dev_status, mx_stream_t stream) {
   bool empty;
-  mx_status st = check_ragged(dd, b, group_offsets, groups, m_total, n, k, dtype, da, &empty);
+  mx_status st = check_ragged(dd, b, group_offsets, groups, m_total, n, k, n, dtype, da, &empty);
   if (st != MX_OK || empty) return st;
   int sms;
   int32_t* status;
@@ -792,7 +797,7 @@ mx_status mx_grouped_gemm_ragged_wgrad(const void* dd, const void* a, const int3
                                        void* db, int32_t* dev_status, mx_stream_t stream) {
   if (out_dtype != dtype && out_dtype != MX_FP32) return MX_ERR_INVALID_ARGUMENT;
   bool empty;
-  mx_status st = check_ragged(dd, a, group_offsets, groups, m_total, n, k, dtype, db, &empty);
+  mx_status st = check_ragged(dd, a, group_offsets, groups, m_total, n, k, m_total, dtype, db, &empty);
   if (st != MX_OK) return st;
   if (empty) {
     if (groups == 0) return MX_OK;

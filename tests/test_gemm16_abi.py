@@ -24,7 +24,7 @@ def test_linear_act(lib):
     assert f(dtype=FP32) == f(dtype=-1) == f(dtype=3) == MX_ERR_INVALID_ARGUMENT
     assert f(act=-1) == f(act=5) == MX_ERR_INVALID_ARGUMENT
     assert f(k=0) == f(k=36) == f(n=20) == MX_ERR_UNSUPPORTED_SHAPE
-    assert f(m=BIG) == f(n=1 << 31) == f(k=1 << 31) == MX_ERR_UNSUPPORTED_SHAPE
+    assert f(m=BIG) == f(n=1 << 31) == f(k=1 << 31) == f(k=(1 << 27) + 8) == MX_ERR_UNSUPPORTED_SHAPE
     assert f(x=None) == f(w=None) == f(y=None) == MX_ERR_INVALID_ARGUMENT
     for name in ("x", "w", "bias", "res", "z", "y"):
         assert f(**{name: FAKE + 8}) == MX_ERR_MISALIGNED
@@ -42,6 +42,7 @@ def test_linear_act_backward(lib):
         return lib.mx_linear_act_backward(dy, z, x, w, dz, dx, dw, db, m, n, k, dtype, act, work, size, None, None)
     assert f(m=-1) == f(dtype=FP32) == f(act=7) == MX_ERR_INVALID_ARGUMENT
     assert f(k=0) == f(k=33) == f(n=9) == f(m=BIG) == MX_ERR_UNSUPPORTED_SHAPE
+    assert f(m=(1 << 27) + 1) == f(n=(1 << 27) + 8) == MX_ERR_UNSUPPORTED_SHAPE   # dw sums over m, dx over n
     assert f(dy=None) == f(z=None) == f(dz=None) == MX_ERR_INVALID_ARGUMENT
     assert f(x=None) == f(w=None) == MX_ERR_INVALID_ARGUMENT            # dw wants x, dx wants w
     big = {"m": 2000, "n": 16}
@@ -75,6 +76,10 @@ def test_grouped_ragged(lib):
         assert f(None, None, None, 0, 4, 16, 32, BF16, None) == MX_OK
     for name in ("forward", "dgrad"):
         assert calls[name](None, None, None, 2, 0, 16, 32, BF16, None) == MX_OK
+    over = (1 << 27) + 8
+    assert calls["forward"](FAKE, FAKE, FAKE, 2, 4, 16, over, BF16, FAKE) == MX_ERR_UNSUPPORTED_SHAPE
+    assert calls["dgrad"](FAKE, FAKE, FAKE, 2, 4, over, 16, BF16, FAKE) == MX_ERR_UNSUPPORTED_SHAPE
+    assert calls["wgrad"](FAKE, FAKE, FAKE, 2, over, 16, 16, BF16, FAKE) == MX_ERR_UNSUPPORTED_SHAPE
     w = lib.mx_grouped_gemm_ragged_wgrad
     assert w(FAKE, FAKE, FAKE, 2, 4, 16, 32, BF16, FP16, FAKE, None, None) == MX_ERR_INVALID_ARGUMENT
     assert w(FAKE, FAKE, FAKE, 2, 4, 16, 32, FP16, BF16, FAKE, None, None) == MX_ERR_INVALID_ARGUMENT

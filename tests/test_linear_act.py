@@ -307,6 +307,17 @@ def test_two_streams_at_once(mx):
                 assert all(torch.equal(a, b) for a, b in zip(run, ref))
 
 
+def test_stream_by_pointer(mx):
+    """The stream may be a raw pointer, and what the call allocates belongs to it."""
+    x, w = normal((300, 264), BF16, 1), normal((136, 264), BF16, 2, 0.1)
+    want = mx.mx_linear_act(x, w, activation="silu")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [mx.mx_linear_act(x, w, activation="silu", stream=side.cuda_stream) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
 def test_wait_timeout_reported(mx):
     """A wait bound far below the kernels' legitimate waits: the call reports
     MX_DEV_TIMEOUT, writes nothing outside its output and leaves the context
