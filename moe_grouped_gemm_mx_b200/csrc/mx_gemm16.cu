@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
             continue;
           }
           float v[64];
+          __syncwarp();  // TMEM loads are the whole warp's
           {
             uint32_t raw[2][32];
             tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw[0]);
@@ -466,6 +467,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
         // 32 columns from `c` of the warp's 64: the accumulator, and this lane's row of the tile
         auto acc32 = [&](int c, float (&v)[32]) {
           uint32_t raw[32];
+          __syncwarp();  // TMEM loads are the whole warp's
           tc_ld_32x32b_x32(t_row + (it & 1u) * kP16TN + c, raw);
           tc_wait_ld();
 #pragma unroll
@@ -809,6 +811,7 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
   }
   // 32 columns of this thread's accumulator row (16 where a CTA has no more)
   auto columns = [&](int col_t, uint32_t (&raw)[32]) {
+    __syncwarp();  // TMEM loads are the whole warp's
     if (width >= 32) {
       tc_ld_32x32b_x32(t_row + col_t, raw);
     } else {

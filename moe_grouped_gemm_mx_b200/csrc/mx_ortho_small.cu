@@ -37,7 +37,6 @@ constexpr int kNsGroups = kNsThreads / 128;
 constexpr int kNsSmem = 232448;
 constexpr int kNsLogSA = 12;     // A and B are held times 2^12
 constexpr int kNsMaxCluster = 16;
-constexpr int kNsTurn = 65;      // 32-bit words between the rows of a turning tile of 16 x 64
 
 struct NsSmallArgs {
   const void* g;
@@ -84,8 +83,10 @@ __device__ __forceinline__ uint32_t kmajor_at(int rows, int row, int k) {
   return static_cast<uint32_t>((k >> 6) * rows * 128 + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) + (k & 7) * 2);
 }
 
-template <typename T>
+// cs: CTAs of the cluster
+template <typename T, int cs>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_constant__ NsSmallArgs args) {
+  static_assert(cs >= 1 && cs <= kNsMaxCluster && 16 % cs == 0, "cluster size");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -93,9 +94,6 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const int wgroup = warp >> 2;                   // which chunks of 64 columns
   const int row = (warp & 3) * 32 + lane;         // TMEM lane and matrix row
   const int rank = static_cast<int>(cluster_ctarank());
-  uint32_t cs_u;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs_u));
-  const int cs = static_cast<int>(cs_u);
   const int batch = static_cast<int>(blockIdx.x) / cs;
 
   const bool tall = args.m > args.n;
@@ -105,19 +103,19 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   // a warp whose 32 rows lie behind the matrix has no chunks
   const int first = (warp & 3) * 32 < rp ? wgroup : chunks, first16 = (warp & 3) * 32 < rp ? wgroup : rp / 16;
   const int c0 = rank * slice;                    // the slice's first column; those at or beyond c are zeros
-  const int w = rp / cs > 0 ? (rp + cs - 1) / cs : 1;  // columns of A this CTA adds up (cs <= 16 divides rp)
+  const int w = rp / cs;                          // columns of A this CTA adds up (cs <= 16 divides rp)
   const uint32_t misc = sbase;                                       // see below
   const uint32_t xs = sbase + 1024;                                  // X, FP16
   const uint32_t as = xs + chunks * rp * 128;                        // A
   const uint32_t bs = as + (rp + 63) / 64 * rp * 128;                // B
   const uint32_t recv = bs + (rp + 63) / 64 * rp * 128;              // [source][column][row] partial sums
-  const uint32_t turn = recv + warp * (16 * kNsTurn * 4);            // this warp's tile for turning rows into lanes
-  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8
+  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8, factors 3 x 4
   const uint32_t bar = misc;
   auto at = [&](uint32_t addr) { return smem + (addr - sbase); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(at(misc + 8));
   double* block_sums = reinterpret_cast<double*>(at(misc + 16));
   const uint32_t cluster_sums = misc + 144;
+  volatile float* factors = reinterpret_cast<volatile float*>(at(misc + 272));
 
   if (tid == 0) {
     mbar_init(bar, 1);
@@ -146,91 +144,48 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   // ---- read: raw values to TMEM, their squares summed in 64 bits over the cluster
   const T* g = static_cast<const T*>(args.g) + static_cast<int64_t>(batch) * args.m * args.n;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  float* tile = reinterpret_cast<float*>(at(turn));
   constexpr int V = 16 / static_cast<int>(sizeof(T));  // values of a 16-byte load
-  const bool wide_loads = !tall && c % V == 0;
   for (int j = first; j < chunks; j += kNsGroups) {
-    const int col = c0 + j * 64, row_w = row - lane;
-    uint32_t raw[64];
-    if (!tall) {
-      // rows as they lie, 16 of the warp's at a time through the turning tile
-      constexpr int LANES = 64 / V, ROWS = 32 / LANES;  // lanes of a row, rows of a load
-      uint4 q[32 / ROWS];
-      uint32_t u16[sizeof(T) == 2 ? 32 : 1];  // unaligned BF16 rows: columns lane and lane + 32
-      if (!wide_loads && sizeof(T) == 2) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(g) + static_cast<int64_t>(row_w) * c + col + lane;
+    // each lane its own row: a warp's loads fall into 32 lines, but every byte of them
+    // is wanted, and the cluster reads a matrix once
+    const int col = c0 + j * 64;
+    uint32_t v[64];
+    if (!tall && c % V == 0) {
+      const uint4* p = reinterpret_cast<const uint4*>(g + static_cast<int64_t>(row) * c + col);
 #pragma unroll
-        for (int i = 0; i < (sizeof(T) == 2 ? 32 : 0); ++i, p += c) {
-          const uint32_t lo = row_w + i < r && col + lane < c ? __ldg(p) : 0u;
-          const uint32_t hi = row_w + i < r && col + lane + 32 < c ? __ldg(p + 32) : 0u;
-          u16[i] = lo | hi << 16;
-        }
-      }
-      if (wide_loads) {
+      for (int q = 0; q < 64 / V; ++q) {
+        const uint4 w4 = row < r && col + q * V < c ? __ldg(p + q) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-        for (int i = 0; i < 32 / ROWS; ++i) {
-          const int y = row_w + i * ROWS + lane / LANES, x = col + lane % LANES * V;
-          q[i] = y < r && x < c ? __ldg(reinterpret_cast<const uint4*>(g + static_cast<int64_t>(y) * c + x)) : make_uint4(0, 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        __syncwarp();  // the tile has been read
-        if (wide_loads) {
-#pragma unroll
-          for (int i = 0; i < 16 / ROWS; ++i) {
-            const uint4 w4 = q[part * (16 / ROWS) + i];
-            const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
-            float* to = tile + (i * ROWS + lane / LANES) * kNsTurn + lane % LANES * V;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              if constexpr (sizeof(T) == 4) {
-                to[p] = __uint_as_float(u[p]);
-              } else {
-                const float2 f2 = unpack16(u[p], 0);
-                to[2 * p] = f2.x;
-                to[2 * p + 1] = f2.y;
-              }
-            }
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) {
+            v[q * 4 + i] = u[i];
+          } else {
+            v[q * 8 + 2 * i] = u[i] << 16;
+            v[q * 8 + 2 * i + 1] = u[i] & 0xFFFF0000u;
           }
-        } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 f2 = unpack16(u16[part * 16 + i], 0);
-            tile[i * kNsTurn + lane] = f2.x;
-            tile[i * kNsTurn + lane + 32] = f2.y;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int y = row_w + part * 16 + i;
-            const T* p = g + static_cast<int64_t>(y) * c + col + lane;
-            tile[i * kNsTurn + lane] = y < r && col + lane < c ? static_cast<float>(p[0]) : 0.0f;
-            tile[i * kNsTurn + lane + 32] = y < r && col + lane + 32 < c ? static_cast<float>(p[32]) : 0.0f;
-          }
-        }
-        __syncwarp();
-        if (lane / 16 == part) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) raw[k] = __float_as_uint(tile[(lane & 15) * kNsTurn + k]);
         }
       }
     } else {
+      const int64_t step = tall ? r : 1;
+      const T* p = g + (tall ? static_cast<int64_t>(col) * r + row : static_cast<int64_t>(row) * c + col);
 #pragma unroll
-      for (int k = 0; k < 64; ++k)
-        raw[k] = row < r && col + k < c
-                     ? __float_as_uint(static_cast<float>(g[static_cast<int64_t>(col + k) * r + row])) : 0u;
+      for (int i = 0; i < 64; ++i) {
+        const float x = row < r && col + i < c ? static_cast<float>(p[i * step]) : 0.0f;
+        v[i] = __float_as_uint(x);
+      }
     }
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
+      uint32_t half[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        v[i] = raw[h * 32 + i];
-        const double x = __uint_as_float(v[i]);
+        half[i] = v[h * 32 + i];
+        const double x = __uint_as_float(half[i]);
         s[i & 3] = fma(x, x, s[i & 3]);
       }
-      tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
+      tc_st_32x32b_x32(t_row + j * 64 + h * 32, half);
     }
   }
   tc_wait_st();
@@ -244,42 +199,54 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     st_cluster_f64(map_to_rank(cluster_sums, tid) + rank * 8, t);
   }
   cluster_sync();
-  double sum = 0.0;
-  for (int i = 0; i < cs; ++i) sum += reinterpret_cast<const double*>(at(cluster_sums))[i];
-  const double f = sqrt(sum) + static_cast<double>(args.eps);
-  const bool usual = f > 0.0 && isfinite(f);  // else: zeros stay zeros, anything else becomes NaN
-  const int e = usual ? ilogb(f) : 0;
-  const float rest = usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("");
+  if (tid == 0) {  // (one thread: the FP64 unit is narrow)
+    double sum = 0.0;
+    for (int i = 0; i < cs; ++i) sum += reinterpret_cast<const double*>(at(cluster_sums))[i];
+    const double f = sqrt(sum) + static_cast<double>(args.eps);
+    const bool usual = f > 0.0 && isfinite(f);  // else: zeros stay zeros, anything else becomes NaN
+    const int e = usual ? ilogb(f) : 0;
+    // 2^(sx - e) in two halves: neither leaves FP32's range
+    const int shift = args.log_sx - e;
+    factors[0] = scalbnf(1.0f, shift / 2);
+    factors[1] = scalbnf(1.0f, shift - shift / 2);
+    factors[2] = (usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("")) * (1 << kNsLogSA);
+  }
+  __syncthreads();
+  const float up0 = factors[0], up1 = factors[1], up2 = factors[2];
   const float sa = static_cast<float>(1 << kNsLogSA), inv_sa = 1.0f / sa;
-  // 2^(sx - e) in two halves: neither leaves FP32's range
-  const int shift = args.log_sx - e;
-  const float up0 = scalbnf(1.0f, shift / 2), up1 = scalbnf(1.0f, shift - shift / 2) , up2 = rest * sa;
 
-  // FP16 copy of 32 columns of X for the products (rows of zeros up to rp)
-  auto put_x = [&](int col, const uint32_t (&v)[32]) {  // v: X 2^(sx + 12)
+  // FP16 copy of a chunk of X for the products (rows of zeros up to rp); v: X 2^(sx + 12)
+  auto put_x = [&](int j, int h, const uint32_t (&v)[32]) {
     if (row >= rp) return;
+    const uint32_t line = xs + j * rp * 128 + row * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         o[i] = pack16(__uint_as_float(v[q * 8 + 2 * i]) * inv_sa, __uint_as_float(v[q * 8 + 2 * i + 1]) * inv_sa, 1);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(xs + kmajor_at(rp, row, col + q * 8)), "r"(o[0]),
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((h * 4 + q) ^ (row & 7)) << 4)), "r"(o[0]),
                    "r"(o[1]), "r"(o[2]), "r"(o[3])
                    : "memory");
     }
   };
+  // 64 columns of X's TMEM row, both halves on their way at once
+  auto load_x = [&](int j, uint32_t (&lo)[32], uint32_t (&hi)[32]) {
+    __syncwarp();  // TMEM loads and stores are the whole warp's
+    tc_ld_32x32b_x32(t_row + j * 64, lo);
+    tc_ld_32x32b_x32(t_row + j * 64 + 32, hi);
+    tc_wait_ld();
+  };
   for (int j = first; j < chunks; j += kNsGroups) {
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
-      tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
-      tc_wait_ld();
+    uint32_t v[2][32];
+    load_x(j, v[0], v[1]);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = __float_as_uint(__uint_as_float(v[i]) * up0 * up1 * up2);
-      tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
-      put_x(j * 64 + h * 32, v);
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[h][i] = __float_as_uint(__uint_as_float(v[h][i]) * up0 * up1 * up2);
+      tc_st_32x32b_x32(t_row + j * 64 + h * 32, v[h]);
+      put_x(j, h, v[h]);
+      __syncwarp();
     }
   }
   tc_wait_st();
@@ -296,9 +263,13 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     __syncthreads();
     if (warp == 0 && elect_one()) {
       tc_fence_after();
-      for (int k = 0; k < slice / 16; ++k) {
-        const uint64_t d = desc_kmajor_sw128(xs + (k >> 2) * rp * 128 + (k & 3) * 32);
-        tc_mma_f16(tmem + t_a, d, d, idesc_r, k != 0 ? 1u : 0u);
+      const int live = c - c0 < slice ? (c - c0 > 0 ? (c - c0 + 63) / 64 : 1) : chunks;  // the others are zeros
+      uint64_t d = desc_kmajor_sw128(xs);
+      for (int j = 0; j < live; ++j, d += rp * 8) {  // descriptors count 16 bytes
+        tc_mma_f16(tmem + t_a, d, d, idesc_r, j != 0 ? 1u : 0u);
+        tc_mma_f16(tmem + t_a, d + 2, d + 2, idesc_r, 1);
+        tc_mma_f16(tmem + t_a, d + 4, d + 4, idesc_r, 1);
+        tc_mma_f16(tmem + t_a, d + 6, d + 6, idesc_r, 1);
       }
       tc_commit(bar);
     }
@@ -308,14 +279,13 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // and a X of one X with B X of another would only add the difference.
     const bool add_x = step == 0 || step + 2 < args.steps;
     for (int j = add_x ? first : chunks; j < chunks; j += kNsGroups) {
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[32];
-        tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
-        tc_wait_ld();
+      uint32_t v[2][32];
+      load_x(j, v[0], v[1]);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(ca * __uint_as_float(v[i]));
-        tc_st_32x32b_x32(t_row + j * 64 + h * 32, v);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[h][i] = __float_as_uint(ca * __uint_as_float(v[h][i]));
+        tc_st_32x32b_x32(t_row + j * 64 + h * 32, v[h]);
       }
     }
     tc_wait_st();
@@ -323,13 +293,20 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // ---- partial sums to the CTAs that add them
     for (int b = first16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
+      __syncwarp();
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
       tc_wait_ld();
       if (row < rp) {
+        int owner = b * 16 / w, q = b * 16 - owner * w;
+        uint32_t to = map_to_rank(recv, owner) + static_cast<uint32_t>(((rank * w + q) * 128 + row) * 4);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int col = b * 16 + i, owner = col / w;
-          st_cluster_b32(map_to_rank(recv, owner) + static_cast<uint32_t>(((rank * w + col - owner * w) * 128 + row) * 4), v[i]);
+          st_cluster_b32(to, v[i]);
+          to += 512;
+          if (++q == w && i < 15) {
+            q = 0;
+            to = map_to_rank(recv, ++owner) + static_cast<uint32_t>((rank * w * 128 + row) * 4);
+          }
         }
       }
     }
@@ -339,10 +316,14 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     if (row < rp) {
       for (int q = wgroup; q < w; q += kNsGroups) {
         const float* p = reinterpret_cast<const float*>(at(recv)) + q * 128 + row;
-        float t = 0.0f;
-        for (int i = 0; i < cs; ++i) t += p[i * w * 128];
+        float part[cs], t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < cs; ++i) part[i] = p[i * w * 128];
+#pragma unroll
+        for (int i = 0; i < cs; ++i) t += part[i];
         const uint16_t v = static_cast<uint16_t>(pack16(t * a_scale, 0.0f, 1) & 0xFFFFu);
         const uint32_t to = as + kmajor_at(rp, rank * w + q, row);
+#pragma unroll
         for (int i = 0; i < cs; ++i) st_cluster_b16(map_to_rank(to, i), v);
       }
     }
@@ -365,6 +346,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // ---- B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)^2 (+ a 2^12 I)
     for (int b = first16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
+      __syncwarp();
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
       tc_wait_ld();
       if (row < rp) {
@@ -405,13 +387,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     wait_mma();
     if (step + 1 < args.steps) {
       for (int j = first; j < chunks; j += kNsGroups) {
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
-          tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
-          tc_wait_ld();
-          put_x(j * 64 + h * 32, v);
-        }
+        uint32_t v[2][32];
+        load_x(j, v[0], v[1]);
+        put_x(j, 0, v[0]);
+        put_x(j, 1, v[1]);
       }
     }
   }
@@ -420,49 +399,23 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const float last = inv_sa * scalbnf(1.0f, -args.log_sx);
   __nv_bfloat16* out = args.out + static_cast<int64_t>(batch) * args.m * args.n;
   for (int j = first; j < chunks; j += kNsGroups) {
-    const int col = c0 + j * 64, row_w = row - lane;
-    uint32_t w2[32];  // pairs of columns
+    const int col = c0 + j * 64;
+    uint32_t v[2][32], o[32];  // o: pairs of columns
+    load_x(j, v[0], v[1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t v[32];
-      tc_ld_32x32b_x32(t_row + j * 64 + h * 32, v);
-      tc_wait_ld();
+    for (int i = 0; i < 32; ++i)
+      o[i] = pack16(__uint_as_float(v[i / 16][i % 16 * 2]) * last, __uint_as_float(v[i / 16][i % 16 * 2 + 1]) * last, 0);
+    if (row < r) {
+      uint16_t* p = reinterpret_cast<uint16_t*>(out) + (tall ? static_cast<int64_t>(col) * r + row : static_cast<int64_t>(row) * c + col);
+      if (!tall && c % 8 == 0) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w2[h * 16 + i] = pack16(__uint_as_float(v[2 * i]) * last, __uint_as_float(v[2 * i + 1]) * last, 0);
-    }
-    if (tall) {
+        for (int q = 0; q < 8; ++q)
+          if (col + q * 8 < c) reinterpret_cast<uint4*>(p)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      } else {
+        const int64_t step = tall ? r : 1;
 #pragma unroll
-      for (int k = 0; k < 64; ++k)
-        if (row < r && col + k < c)
-          reinterpret_cast<uint16_t*>(out)[static_cast<int64_t>(col + k) * r + row] = static_cast<uint16_t>(w2[k / 2] >> (k & 1) * 16);
-    } else {
-      // 16 rows of 32 pairs at a time through the turning tile
-      uint32_t* pairs = reinterpret_cast<uint32_t*>(tile);
-      constexpr int STEP = kNsTurn / 2 + 1;  // 33
-      static_assert(16 * STEP <= 16 * kNsTurn, "the tile holds them");
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        __syncwarp();
-        if (lane / 16 == part) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) pairs[(lane & 15) * STEP + k] = w2[k];
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int y = row_w + part * 16 + i, x = col + 2 * lane;
-          const uint32_t u = pairs[i * STEP + lane];
-          uint16_t* o = reinterpret_cast<uint16_t*>(out) + static_cast<int64_t>(y) * c + x;
-          if (y < r && x < c) {
-            if (c % 2 == 0) {
-              *reinterpret_cast<uint32_t*>(o) = u;
-            } else {
-              o[0] = static_cast<uint16_t>(u);
-              if (x + 1 < c) o[1] = static_cast<uint16_t>(u >> 16);
-            }
-          }
-        }
+        for (int k = 0; k < 64; ++k)
+          if (col + k < c) p[k * step] = static_cast<uint16_t>(o[k / 2] >> (k & 1) * 16);
       }
     }
   }
@@ -480,6 +433,19 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
 
 constexpr int kNsDevices = 64;
 
+using NsKernel = void (*)(NsSmallArgs);
+
+template <typename T>
+static NsKernel ns_kernel(int cs) {
+  switch (cs) {
+    case 1: return ns_cluster_kernel<T, 1>;
+    case 2: return ns_cluster_kernel<T, 2>;
+    case 4: return ns_cluster_kernel<T, 4>;
+    case 8: return ns_cluster_kernel<T, 8>;
+    default: return ns_cluster_kernel<T, 16>;
+  }
+}
+
 // Clusters of `cs` CTAs that the GPU holds at once (0: none).
 template <typename T>
 static int ns_clusters(int cs) {
@@ -489,6 +455,7 @@ static int ns_clusters(int cs) {
   int v = known[dev][cs].load(std::memory_order_acquire);
   if (v == 0) {
     int n = 0;
+    const NsKernel kernel = ns_kernel<T>(cs);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
@@ -500,9 +467,9 @@ static int ns_clusters(int cs) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess ||
-        cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, ns_cluster_kernel<T>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -519,9 +486,10 @@ static bool ns_fits(int r, int slice, int cs) {
   const int rp = (r + 15) / 16 * 16;
   if (slice + rp > 512) return false;
   const int operands = 1024 + slice / 64 * rp * 128 + 2 * ((rp + 63) / 64) * rp * 128;
-  const int partial = rp * 512, turn = kNsThreads / 32 * 16 * kNsTurn * 4;
-  // (behind B, the products' 128-row operands read (128 - rp) rows more: less than the turning tiles)
-  return 1024 + operands + (partial > turn ? partial : turn) <= kNsSmem;
+  // behind B there are the partial sums, and room for the (128 - rp) rows that the
+  // products' 128-row operands read past B's end
+  const int behind = rp * 512 > (128 - rp) * 128 ? rp * 512 : (128 - rp) * 128;
+  return 1024 + operands + behind <= kNsSmem;
 }
 
 template <typename T>
@@ -567,7 +535,7 @@ static cudaError_t ns_small(const OrthoProblem& q, bool* taken, int num_sms, cud
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ns_cluster_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, ns_kernel<T>(cs), a);
 }
 
 cudaError_t launch_orthogonalize_small(const OrthoProblem& q, bool* taken, int num_sms, cudaStream_t stream) {
