@@ -83,6 +83,49 @@ __device__ __forceinline__ uint32_t kmajor_at(int rows, int row, int k) {
   return static_cast<uint32_t>((k >> 6) * rows * 128 + row * 128 + ((((k & 63) >> 3) ^ (row & 7)) << 4) + (k & 7) * 2);
 }
 
+// 128 bytes from `from` (any address) as 32 words, of which the first `bytes` are
+// wanted: nine 16-byte loads and a shift by what `from` lies behind a multiple of 16.
+// (Loads of an element each would go to L2 one by one: with all of the SM's memory
+// shared there is no L1 to speak of.)  Nothing at or behind `end` is read.
+template <int SIZE>
+__device__ __forceinline__ void load_line(const uint8_t* from, int bytes, const uint8_t* end, uint32_t (&w)[32]) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from) & 15u);
+  const uint8_t* base = from - off;
+  uint32_t v[36];
+#pragma unroll
+  for (int b = 0; b < 9; ++b) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (bytes > 0 && b * 16 < static_cast<int>(off) + bytes) {
+      if (base + b * 16 + 16 <= end) {
+        q = __ldg(reinterpret_cast<const uint4*>(base + b * 16));
+      } else {  // the tensor's last bytes
+        uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 16; i += SIZE) {
+          if (base + b * 16 + i < end) {
+            if constexpr (SIZE == 4)
+              u[i / 4] = __ldg(reinterpret_cast<const uint32_t*>(base + b * 16 + i));
+            else
+              u[i / 4] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(base + b * 16 + i))) << (i & 2) * 8;
+          }
+        }
+        q = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+    v[4 * b] = q.x;
+    v[4 * b + 1] = q.y;
+    v[4 * b + 2] = q.z;
+    v[4 * b + 3] = q.w;
+  }
+  const bool by8 = off & 8, by4 = off & 4, by2 = off & 2;
+#pragma unroll
+  for (int i = 0; i < 34; ++i) v[i] = by8 ? v[i + 2] : v[i];
+#pragma unroll
+  for (int i = 0; i < 33; ++i) v[i] = by4 ? v[i + 1] : v[i];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = SIZE == 2 && by2 ? __funnelshift_r(v[i], v[i + 1], 16) : v[i];
+}
+
 // cs: CTAs of the cluster
 template <typename T, int cs>
 __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_constant__ NsSmallArgs args) {
@@ -144,34 +187,49 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   // ---- read: raw values to TMEM, their squares summed in 64 bits over the cluster
   const T* g = static_cast<const T*>(args.g) + static_cast<int64_t>(batch) * args.m * args.n;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  constexpr int V = 16 / static_cast<int>(sizeof(T));  // values of a 16-byte load
+  const bool aligned = c % (16 / static_cast<int>(sizeof(T))) == 0;  // every row starts on 16 bytes
   for (int j = first; j < chunks; j += kNsGroups) {
     // each lane its own row: a warp's loads fall into 32 lines, but every byte of them
     // is wanted, and the cluster reads a matrix once
     const int col = c0 + j * 64;
     uint32_t v[64];
-    if (!tall && c % V == 0) {
-      const uint4* p = reinterpret_cast<const uint4*>(g + static_cast<int64_t>(row) * c + col);
+    if (!tall) {
+      const int there = row < r && col < c ? (c - col < 64 ? c - col : 64) : 0;  // columns of the chunk
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(g + static_cast<int64_t>(row) * c + col);
+      const uint8_t* end = reinterpret_cast<const uint8_t*>(static_cast<const T*>(args.g) +
+                                                            static_cast<int64_t>(gridDim.x / cs) * args.m * args.n);
 #pragma unroll
-      for (int q = 0; q < 64 / V; ++q) {
-        const uint4 w4 = row < r && col + q * V < c ? __ldg(p + q) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
+      for (int h = 0; h < (sizeof(T) == 4 ? 2 : 1); ++h) {
+        constexpr int N = 128 / sizeof(T);
+        const int n = there - h * N < 0 ? 0 : there - h * N < N ? there - h * N : N;
+        uint32_t w32[32];
+        if (aligned) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+          for (int q = 0; q < 8; ++q) {
+            const uint4 u = q * (N / 8) < n ? __ldg(reinterpret_cast<const uint4*>(p + h * 128) + q) : make_uint4(0, 0, 0, 0);
+            w32[4 * q] = u.x;
+            w32[4 * q + 1] = u.y;
+            w32[4 * q + 2] = u.z;
+            w32[4 * q + 3] = u.w;
+          }
+        } else {
+          load_line<sizeof(T)>(p + h * 128, n * static_cast<int>(sizeof(T)), end, w32);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
           if constexpr (sizeof(T) == 4) {
-            v[q * 4 + i] = u[i];
+            v[h * 32 + i] = i < n ? w32[i] : 0u;
           } else {
-            v[q * 8 + 2 * i] = u[i] << 16;
-            v[q * 8 + 2 * i + 1] = u[i] & 0xFFFF0000u;
+            v[2 * i] = 2 * i < n ? w32[i] << 16 : 0u;
+            v[2 * i + 1] = 2 * i + 1 < n ? w32[i] & 0xFFFF0000u : 0u;
           }
         }
       }
     } else {
-      const int64_t step = tall ? r : 1;
-      const T* p = g + (tall ? static_cast<int64_t>(col) * r + row : static_cast<int64_t>(row) * c + col);
+      const T* p = g + static_cast<int64_t>(col) * r + row;
 #pragma unroll
       for (int i = 0; i < 64; ++i) {
-        const float x = row < r && col + i < c ? static_cast<float>(p[i * step]) : 0.0f;
+        const float x = row < r && col + i < c ? static_cast<float>(p[static_cast<int64_t>(i) * r]) : 0.0f;
         v[i] = __float_as_uint(x);
       }
     }
@@ -407,15 +465,26 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
       o[i] = pack16(__uint_as_float(v[i / 16][i % 16 * 2]) * last, __uint_as_float(v[i / 16][i % 16 * 2 + 1]) * last, 0);
     if (row < r) {
       uint16_t* p = reinterpret_cast<uint16_t*>(out) + (tall ? static_cast<int64_t>(col) * r + row : static_cast<int64_t>(row) * c + col);
-      if (!tall && c % 8 == 0) {
+      if (tall) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (col + k < c) p[static_cast<int64_t>(k) * r] = static_cast<uint16_t>(o[k / 2] >> (k & 1) * 16);
+      } else if (c % 8 == 0) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (col + q * 8 < c) reinterpret_cast<uint4*>(p)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      } else {
-        const int64_t step = tall ? r : 1;
+      } else {  // pairs on 4 bytes: of a row that starts between them from its second value on
+        const int there = c - col < 64 ? c - col : 64, odd = reinterpret_cast<uintptr_t>(p) & 2 ? 1 : 0;
+        if (odd && there > 0) p[0] = static_cast<uint16_t>(o[0]);
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (col + k < c) p[k * step] = static_cast<uint16_t>(o[k / 2] >> (k & 1) * 16);
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t pair = odd ? (i < 31 ? __funnelshift_r(o[i], o[i + 1], 16) : o[i] >> 16) : o[i];
+          const int at2 = 2 * i + odd;
+          if (at2 + 1 < there)
+            *reinterpret_cast<uint32_t*>(p + at2) = pair;
+          else if (at2 < there)
+            p[at2] = static_cast<uint16_t>(pair);
+        }
       }
     }
   }
