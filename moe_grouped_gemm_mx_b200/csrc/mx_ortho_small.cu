@@ -11,7 +11,7 @@
 //   A     each CTA multiplies its slice's X X^T (K = slice), the partial sums meet in
 //         distributed shared memory, each CTA adds some columns (in rank order), and
 //         everyone receives all of A 2^12 as FP16;
-//   B     = b A + c A^2 in every CTA;
+//   B     = b A + c A^2 in every CTA, as the sum of two FP16 numbers;
 //   X     <- a X + B X: TMEM times a while the partial sums are formed, then the
 //         product accumulates onto it.
 // The chunk of 64 columns of X in shared memory is at the same time a K-major
@@ -401,7 +401,10 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     }
     __syncwarp();
     wait_mma();
-    // ---- B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)^2 (+ a 2^12 I)
+    // ---- B 2^12 = b (A 2^12) + c 2^-12 (A 2^12)^2 (+ a 2^12 I), and what its rounding
+    // leaves in A's place (A^2 is done, each entry of A is read by the lane that
+    // writes there): near the fixed point a and B cancel to a fifth, and B's rounding
+    // was half the method's error
     for (int b = first16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
       __syncwarp();
@@ -413,16 +416,21 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
           const uint32_t where = kmajor_at(rp, row, b * 16 + q * 8);
           const uint4 a4 = *reinterpret_cast<const uint4*>(at(as + where));
           const uint32_t u[4] = {a4.x, a4.y, a4.z, a4.w};
-          uint32_t o[4];
+          uint32_t o[4], l[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 af = unpack16(u[i], 1);
             const int col = b * 16 + q * 8 + 2 * i;
             const float d0 = !add_x && col == row ? ca * sa : 0.0f, d1 = !add_x && col + 1 == row ? ca * sa : 0.0f;
-            o[i] = pack16(fmaf(cb, af.x, fmaf(__uint_as_float(v[q * 8 + 2 * i]), cc * inv_sa, d0)),
-                          fmaf(cb, af.y, fmaf(__uint_as_float(v[q * 8 + 2 * i + 1]), cc * inv_sa, d1)), 1);
+            const float b0 = fmaf(cb, af.x, fmaf(__uint_as_float(v[q * 8 + 2 * i]), cc * inv_sa, d0));
+            const float b1 = fmaf(cb, af.y, fmaf(__uint_as_float(v[q * 8 + 2 * i + 1]), cc * inv_sa, d1));
+            o[i] = pack16(b0, b1, 1);
+            const float2 h = unpack16(o[i], 1);
+            l[i] = pack16(b0 - h.x, b1 - h.y, 1);
           }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(bs + where), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(as + where), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3])
                        : "memory");
         }
       }
@@ -435,9 +443,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
       tc_fence_after();
       for (int n0 = 0; n0 < slice; n0 += 256) {
         const uint32_t idesc = idesc_f16(128, slice - n0 < 256 ? slice - n0 : 256, 1, 0, 1);
-        for (int k = 0; k < rp / 16; ++k)
-          tc_mma_f16(tmem + n0, desc_kmajor_sw128(bs + (k >> 2) * rp * 128 + (k & 3) * 32),
-                     desc_mnmajor_sw128(xs + (n0 / 64) * rp * 128 + k * 2048, rp * 128), idesc, add_x || k != 0 ? 1u : 0u);
+        for (int k = 0; k < rp / 16; ++k) {
+          const uint64_t x = desc_mnmajor_sw128(xs + (n0 / 64) * rp * 128 + k * 2048, rp * 128);
+          const uint32_t at_k = (k >> 2) * rp * 128 + (k & 3) * 32;
+          tc_mma_f16(tmem + n0, desc_kmajor_sw128(bs + at_k), x, idesc, add_x || k != 0 ? 1u : 0u);
+          tc_mma_f16(tmem + n0, desc_kmajor_sw128(as + at_k), x, idesc, 1);
+        }
       }
       tc_commit(bar);
     }
