@@ -509,7 +509,7 @@ mx_status mx_linear_act(const void *x, const void *w, const void *bias, const vo
  * it needs `workspace` of mx_linear_act_backward_workspace_bytes(m, n) bytes (none
  * up to m = 1024).
  * ReLU's derivative at zero is 0.  x is read for dw only, w for dx only (NULL
- * otherwise).  m == 0 gives zero dw and dbias; n == 0 gives zero dx.
+ * otherwise).  Outputs overlap no input and one another nowhere.  m == 0 gives zero dw and dbias; n == 0 gives zero dx.
  */
 size_t mx_linear_act_backward_workspace_bytes(int64_t m, int64_t n);
 mx_status mx_linear_act_backward(const void *dy, const void *z, const void *x, const void *w, void *dz, void *dx,

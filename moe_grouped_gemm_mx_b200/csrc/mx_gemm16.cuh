@@ -338,10 +338,10 @@ __device__ __forceinline__ float act_f32(float z, int act) {
   }
 }
 
-// act'(z)
+// act'(z), finite for every finite z.  relu passes on what a NaN z gets.
 __device__ __forceinline__ float act_grad_f32(float z, int act) {
   switch (act) {
-    case 1: return z > 0.0f ? 1.0f : 0.0f;
+    case 1: return z <= 0.0f ? 0.0f : 1.0f;
     case 2: {
       const float p = sigmoid_f32(z);
       return p * (1.0f + z * (1.0f - p));
@@ -349,7 +349,8 @@ __device__ __forceinline__ float act_grad_f32(float z, int act) {
     case 3: return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
     case 4: {
       const float p = sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
-      return p + z * p * (1.0f - p) * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+      const float q = p * (1.0f - p);  // 0 long before z^2 overflows
+      return q == 0.0f ? p : p + z * q * 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
     }
     default: return 1.0f;
   }

@@ -4,6 +4,8 @@ every activation, bias, residual and pre-activation, gradients against the
 formulas and against differences, captured graphs and two streams at once."""
 import contextlib
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -285,6 +287,88 @@ def test_captured_and_replayed(mx):
         torch.cuda.synchronize()
         for got, ref in zip(out, want):
             assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_over_the_whole_range(mx, dtype, act):
+    """y and dz for z from the type's smallest to its largest numbers.  A product
+    with one term is exact, so z is.  y is off by its rounding and 2^-19 |z| (the
+    activation's evaluation), dz by its rounding and 2^-19 (the derivative's, at
+    most 1.13 large); results below 2^-126 may become zero."""
+    top = torch.finfo(dtype).max
+    e = torch.arange(-24 if dtype is FP16 else -120, 15 if dtype is FP16 else 127, dtype=torch.float64)
+    mags = torch.cat([torch.zeros(1, dtype=torch.float64), 2.0 ** e, 1.375 * 2.0 ** e[2:-1],
+                      torch.tensor([top, 5.5, 9.0, 13.0, 30.0, 100.0], dtype=torch.float64)])
+    mags = mags.to(dtype)
+    vals = torch.cat([mags, -mags])
+    vals = torch.cat([vals, vals.new_zeros((-len(vals)) % 8)]).cuda()
+    n = len(vals)
+    x = torch.zeros(1, 8, dtype=dtype, device="cuda")
+    x[0, 0] = 1
+    w = torch.zeros(n, 8, dtype=dtype, device="cuda")
+    w[:, 0] = vals
+    y, z = mx.mx_linear_act(x, w, activation=act, return_z=True)
+    assert torch.equal(z[0], vals)
+    zd = vals.double()
+    inner = zd.clamp(-1e4, 1e4)  # (beyond it every activation is z or 0, its slope 1 or 0)
+    ref, slope = act_ref(inner, act)
+    ref = torch.where(zd > 1e4, zd, torch.where(zd < -1e4, torch.zeros_like(zd), ref))
+    u = U[dtype]
+    close(y[0], ref, u * ref.abs() + 2.0 ** -19 * zd.abs() + TINY[dtype] + 2.0 ** -126, f"y {act}")
+    dz = torch.empty(1, n, dtype=dtype, device="cuda")
+    mx.mx_linear_act_backward(torch.ones(1, n, dtype=dtype, device="cuda"), x, None, z=z, activation=act, dz=dz)
+    close(dz[0], slope, u * slope.abs() + 2.0 ** -19 + TINY[dtype], f"dz {act}")
+
+
+def test_relu_passes_on_what_a_nan_gets(mx):
+    z = torch.tensor([[float("nan"), 1.0, -1.0, 0.0, float("inf"), float("-inf"), -0.0, 2.0]], dtype=BF16, device="cuda")
+    dy = torch.arange(1, 9, dtype=torch.float32, device="cuda").to(BF16).view(1, 8)
+    dz = torch.empty_like(dy)
+    mx.mx_linear_act_backward(dy, torch.ones(1, 8, dtype=BF16, device="cuda"), None, z=z, activation="relu", dz=dz)
+    assert dz[0].tolist() == [1, 2, 0, 0, 5, 0, 0, 8]
+
+
+FIRST_CALL = """
+import sys
+import torch
+import moe_grouped_gemm_mx_b200 as mx
+torch.manual_seed(0)
+x = torch.randn(256, 512, device="cuda").bfloat16()
+w = torch.randn(264, 512, device="cuda").bfloat16()
+b = torch.randn(4, 264, 512, device="cuda").bfloat16()
+off = torch.tensor([0, 60, 60, 200, 256], dtype=torch.int32, device="cuda")
+g = torch.randn(2, 32, 700, device="cuda")
+calls = {
+    "linear": lambda: [mx.mx_linear_act(x, w, activation="silu")],
+    "backward": lambda: list(mx.mx_linear_act_backward(x @ w.T, x, w, bias_grad=True)),
+    "ragged": lambda: [mx.mx_grouped_gemm_ragged(x, b, off)],
+    "wgrad": lambda: [mx.mx_grouped_gemm_ragged_wgrad(x, x, off, out_dtype=torch.float32)],
+    "orthogonalize": lambda: [mx.mx_orthogonalize(g)],
+    "general": lambda: [mx.mx_orthogonalize(x)],
+}
+call = calls[sys.argv[1]]
+x @ w.T  # the library's own handles exist before the capture
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call()
+graph.replay()
+torch.cuda.synchronize()
+assert mx.read_internal_status() == 0
+for a, e in zip(got, call()):
+    assert torch.equal(a, e), (a - e).abs().max()
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("which", ["linear", "backward", "ragged", "wgrad", "orthogonalize", "general"])
+def test_first_call_of_a_process_is_captured(mx, which):
+    """What a first call sets up on the host (kernel attributes, the internal
+    status word, what the choice of a kernel asks the device) is allowed in a capture."""
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL, which], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0 and "ok" in done.stdout, done.stdout[-2000:] + done.stderr[-2000:]
 
 
 def test_two_streams_at_once(mx):
