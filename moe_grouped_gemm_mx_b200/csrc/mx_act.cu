@@ -16,17 +16,16 @@
 
 namespace mxk {
 
-constexpr int kActCols = 64;   // columns of a block: 8 threads of 8
-constexpr int kActRows = 32;   // rows a block works on at one time
-
-template <int ACT>
+// COLS: columns of a block, COLS / 8 threads of eight.
+template <int ACT, int COLS, int FP16>
 __global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __restrict__ dy,
                                                            const uint16_t* __restrict__ z, uint16_t* __restrict__ dz,
                                                            float* __restrict__ partial, uint16_t* __restrict__ dbias,
-                                                           int64_t m, int n, int64_t chunk, int fp16) {
-  __shared__ float sums[kActRows][kActCols + 1];
-  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-  const int col = blockIdx.x * kActCols + tx * 8;
+                                                           int64_t m, int n, int64_t chunk) {
+  constexpr int ROWS = 256 * 8 / COLS;  // rows a block works on at one time
+  __shared__ float sums[ROWS][COLS + 1];
+  const int tx = threadIdx.x % (COLS / 8), ty = threadIdx.x / (COLS / 8);
+  const int col = blockIdx.x * COLS + tx * 8;
   const int64_t r0 = blockIdx.y * chunk;
   const int64_t r1 = r0 + chunk < m ? r0 + chunk : m;
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -34,17 +33,17 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __res
   pdl_wait_prior();
   if (col < n) {
 #pragma unroll 4
-    for (int64_t r = r0 + ty; r < r1; r += kActRows) {
+    for (int64_t r = r0 + ty; r < r1; r += ROWS) {
       const int64_t at = r * n + col;
       float g[8];
-      load8(dy + at, fp16, g);
+      load8(dy + at, FP16, g);
       if constexpr (ACT != 0) {
         float x[8];
-        load8(z + at, fp16, x);
+        load8(z + at, FP16, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] *= act_grad_f32(x[j], ACT);
-        *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack16(g[0], g[1], fp16), pack16(g[2], g[3], fp16),
-                                                        pack16(g[4], g[5], fp16), pack16(g[6], g[7], fp16));
+        *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack16(g[0], g[1], FP16), pack16(g[2], g[3], FP16),
+                                                        pack16(g[4], g[5], FP16), pack16(g[6], g[7], FP16));
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] += g[j];
@@ -54,15 +53,20 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const uint16_t* __res
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[ty][tx * 8 + j] = s[j];
   __syncthreads();
-  const int c = blockIdx.x * kActCols + threadIdx.x;
-  if (threadIdx.x < kActCols && c < n) {
-    float t = 0.0f;
+  // a quarter of a warp (COLS 64: all of it alone) adds a column's ROWS sums
+  constexpr int PARTS = 256 / COLS < 8 ? 256 / COLS : 8;
+  const int c = threadIdx.x / PARTS, part = threadIdx.x % PARTS;
+  float t = 0.0f;
+  if (c < COLS)
+    for (int i = part; i < ROWS; i += PARTS) t += sums[i][c];
 #pragma unroll
-    for (int i = 0; i < kActRows; ++i) t += sums[i][threadIdx.x];
+  for (int o = PARTS / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+  const int to = blockIdx.x * COLS + c;
+  if (c < COLS && part == 0 && to < n) {
     if (gridDim.y == 1)
-      dbias[c] = static_cast<uint16_t>(pack16(t, 0.0f, fp16) & 0xFFFFu);
+      dbias[to] = static_cast<uint16_t>(pack16(t, 0.0f, FP16) & 0xFFFFu);
     else
-      partial[static_cast<int64_t>(blockIdx.y) * n + c] = t;
+      partial[static_cast<int64_t>(blockIdx.y) * n + to] = t;
   }
 }
 
@@ -105,26 +109,36 @@ int64_t act_backward_chunks(int64_t m) {
   return c < 64 ? c : 64;
 }
 
+using ActKernel = void (*)(const uint16_t*, const uint16_t*, uint16_t*, float*, uint16_t*, int64_t, int, int64_t);
+
+template <int COLS, int FP16>
+static ActKernel act_kernel(int act) {
+  switch (act) {
+    case 0: return act_backward_kernel<0, COLS, FP16>;
+    case 1: return act_backward_kernel<1, COLS, FP16>;
+    case 2: return act_backward_kernel<2, COLS, FP16>;
+    case 3: return act_backward_kernel<3, COLS, FP16>;
+    default: return act_backward_kernel<4, COLS, FP16>;
+  }
+}
+
 cudaError_t launch_act_backward(const void* dy, const void* z, void* dz, void* dbias, float* partial, int64_t m,
                                 int64_t n, int act, int fp16, cudaStream_t stream) {
   const int64_t chunks = act_backward_chunks(m);
   const int64_t chunk = (m + chunks - 1) / chunks;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((n + kActCols - 1) / kActCols),
+  const bool narrow = chunks == 1;
+  const int cols = narrow ? 16 : 64;
+  cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>((n + cols - 1) / cols),
                                            static_cast<unsigned>((m + chunk - 1) / chunk), 1),
                                       256, stream, attr);
   const uint16_t* y16 = static_cast<const uint16_t*>(dy);
   const uint16_t* z16 = static_cast<const uint16_t*>(z);
   uint16_t* d16 = static_cast<uint16_t*>(dz);
   uint16_t* db = static_cast<uint16_t*>(dbias);
-  cudaError_t e;
-  switch (act) {
-    case 0: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<0>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
-    case 1: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<1>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
-    case 2: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<2>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
-    case 3: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<3>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
-    default: e = cudaLaunchKernelEx(&cfg, act_backward_kernel<4>, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk, fp16); break;
-  }
+  const ActKernel kernel = narrow ? (fp16 ? act_kernel<16, 1>(act) : act_kernel<16, 0>(act))
+                                  : (fp16 ? act_kernel<64, 1>(act) : act_kernel<64, 0>(act));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, y16, z16, d16, partial, db, m, static_cast<int>(n), chunk);
   if (e != cudaSuccess || !dbias || m <= chunk) return e;
   cfg = pdl_config(dim3(static_cast<unsigned>((n + 31) / 32), 1, 1), 256, stream, attr);
   return cudaLaunchKernelEx(&cfg, bias_sum_kernel, static_cast<const float*>(partial), db,

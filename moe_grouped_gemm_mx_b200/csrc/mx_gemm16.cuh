@@ -302,11 +302,26 @@ __device__ __forceinline__ void load8(const void* p, int fp16, float (&f)[8]) {
 
 // ---------------------------------------------------------------- activations
 
+// 2^x and 1/x as the special function unit gives them, results below 2^-126 zero
+// (without that, each costs a scaling of small numbers that no activation needs).
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
 // The logistic function through the exponential of a non-positive number, so
 // that neither the exponential nor the quotient overflows.
 __device__ __forceinline__ float sigmoid_f32(float x) {
-  const float t = __expf(-fabsf(x));
-  const float r = __fdividef(1.0f, 1.0f + t);
+  const float t = exp2_ftz(-kLog2E * fabsf(x));
+  const float r = rcp_ftz(1.0f + t);
   return x >= 0.0f ? r : t * r;
 }
 
@@ -315,15 +330,15 @@ constexpr float kGeluA = 0.044715f;
 
 // Phi(z) = erfc(-z / sqrt 2) / 2 by the approximation 7.1.26 of Abramowitz and
 // Stegun, erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2) with t = 1 / (1 + p x), within
-// 1.5e-7.
-__device__ __forceinline__ float normal_cdf_f32(float z) {
-  const float x = fabsf(z) * 0.7071067811865476f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float half = 0.5f * p * t * __expf(-x * x);  // Phi(-|z|)
+// 1.5e-7.  e: e^(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf_f32(float z, float& e) {
+  const float t = rcp_ftz(fmaf(0.3275911f * 0.7071067811865476f, fabsf(z), 1.0f));
+  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, 0.5f * -0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f);
+  e = exp2_ftz(-0.5f * kLog2E * z * z);
+  const float half = p * t * e;  // Phi(-|z|)
   return z >= 0.0f ? 1.0f - half : half;
 }
 
@@ -332,7 +347,10 @@ __device__ __forceinline__ float act_f32(float z, int act) {
   switch (act) {
     case 1: return z < 0.0f ? 0.0f : z;
     case 2: return z * sigmoid_f32(z);
-    case 3: return z * normal_cdf_f32(z);
+    case 3: {
+      float e;
+      return z * normal_cdf_f32(z, e);
+    }
     case 4: return z * sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
     default: return z;
   }
@@ -346,7 +364,11 @@ __device__ __forceinline__ float act_grad_f32(float z, int act) {
       const float p = sigmoid_f32(z);
       return p * (1.0f + z * (1.0f - p));
     }
-    case 3: return 0.5f * (1.0f + erff(z * 0.7071067811865476f)) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
+    case 3: {  // Phi(z) + z e^(-z^2 / 2) / sqrt(2 pi): one exponential for both
+      float e;
+      const float cdf = normal_cdf_f32(z, e);
+      return fmaf(z * 0.3989422804014327f, e, cdf);
+    }
     case 4: {
       const float p = sigmoid_f32(2.0f * kGeluC * (z + kGeluA * z * z * z));
       const float q = p * (1.0f - p);  // 0 long before z^2 overflows
