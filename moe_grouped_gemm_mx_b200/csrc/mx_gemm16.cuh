@@ -317,13 +317,8 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-// The logistic function through the exponential of a non-positive number, so
-// that neither the exponential nor the quotient overflows.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  const float t = exp2_ftz(-kLog2E * fabsf(x));
-  const float r = rcp_ftz(1.0f + t);
-  return x >= 0.0f ? r : t * r;
-}
+// The logistic function: the exponential's infinity for very negative x gives zero.
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_ftz(1.0f + exp2_ftz(-kLog2E * x)); }
 
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
