@@ -688,7 +688,7 @@ mx_status mx_linear_act(const void* x, const void* w, const void* bias, const vo
   st = launch_context(dev_status, &sms, &status);
   if (st != MX_OK) return st;
   mxk::Gemm16 g = dense16(x, 0, w, 0, y, m, n, k, dtype, status);
-  g.epi = 1;
+  g.epi = bias || residual || z || act != MX_ACT_NONE ? 1 : 0;
   g.bias = bias;
   g.res = residual;
   g.res_ld = n;

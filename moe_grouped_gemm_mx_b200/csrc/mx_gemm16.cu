@@ -606,7 +606,10 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
 
 // ======================================================================= one-CTA split-K kernel
 
-constexpr int kS16Threads = 192;  // producer, MMA, 4 epilogue warps
+// Producer, MMA and the epilogue's warps: eight, so that a whole or half tile's
+// columns are shared by two to a lane quarter (128x128x64 5.7 -> 4.6 us); four where a
+// CTA finishes a quarter or less.
+__host__ __device__ constexpr int s16_threads(int splits) { return splits <= 2 ? 320 : 192; }
 constexpr int kS16T = 128;        // tile rows and columns
 constexpr int kS16K = 64;
 
@@ -614,6 +617,8 @@ constexpr int kS16K = 64;
 // operands of as many K chunks in flight either way).
 template <int STAGES>
 struct S16Layout {
+  static constexpr int STG_BYTES = 32 * 64;  // a staging tile of an epilogue warp: 32 rows of 32 columns
+  static constexpr int OFF_STG = 65536;      // behind the partial sums
   static constexpr int OP_BYTES = 128 * 128;  // 16 KB
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * OP_BYTES;
@@ -626,7 +631,7 @@ struct S16Layout {
   static constexpr int ALLOC = BYTES + 1024;
   // partial sums of the other CTAs (at most 7 slices of 16 columns x 128 rows,
   // or 1 of 64) take the operand ring's place once the MMAs are done
-  static_assert(7 * 16 * 128 * 4 <= OFF_BAR && 64 * 128 * 4 <= OFF_BAR, "reduction buffer");
+  static_assert(7 * 16 * 128 * 4 <= OFF_STG && OFF_STG + 8 * STG_BYTES <= OFF_BAR, "reduction buffer and staging tiles");
   static_assert((STAGES <= 3 ? 2 : 1) * ALLOC <= 232448, "shared memory budget");
 };
 
@@ -774,121 +779,163 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
     }
     __syncwarp();
   }
-  bool got = true;
-  const int quarter = warp & 3;
-  const int r = quarter * 32 + lane;
-  const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-  const int row = tl.row0 + r;
-  const bool valid = row < tl.rows_end;
-  const int width = kS16T / splits;  // columns of the tile this CTA finishes
-  const int col_p = tl.nb * kS16T + part * width;
-  const int col_end = col_p + width < args.n ? col_p + width : args.n;
-  // what the epilogue reads comes while the operands do: C and the residual into
-  // registers, the bias as FP32 into shared memory
-  uint4 res[4][4], low[4][4];
-  if (warp >= 2) {
+  if (warp < 2) {
+    if (splits > 1) {  // the epilogue warps' exchange of partial sums
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ===== epilogue: a warp has the rows of a TMEM lane quarter and some of the columns
+    const int ew = warp - 2, grp = ew >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int row_w = tl.row0 + quarter * 32;  // the warp's first row
+    const int row = row_w + lane;
+    const bool valid = row < tl.rows_end;
+    const int width = kS16T / splits;          // columns of the tile this CTA finishes
+    const int grps = splits <= 2 ? 2 : 1;      // warps of a quarter
+    const int wcols = width / grps;            // columns of this warp
+    const int wc = grp * wcols;
+    const int col_w = tl.nb * kS16T + part * width + wc;
+    const int col_end = col_w + wcols < args.n ? col_w + wcols : args.n;
+    // what the epilogue reads comes while the operands do: C and the residual into
+    // registers, the bias as FP32 into shared memory
+    uint4 res[2][4];
     if constexpr (EPI == kEpiLinear) {
-      if (args.bias != nullptr && col_p + r < col_end) {
-        const uint16_t b = __ldg(static_cast<const uint16_t*>(args.bias) + col_p + r);
-        bias[r] = unpack16(b, args.op_fp16).x;
-      }
-      named_barrier_sync(1, 128);
+      const int j = threadIdx.x - 64, col = tl.nb * kS16T + part * width + j;
+      if (args.bias != nullptr && j < width && col < args.n)
+        bias[j] = unpack16(__ldg(static_cast<const uint16_t*>(args.bias) + col), args.op_fp16).x;
+      named_barrier_sync(1, s16_threads(splits) - 64);
     }
     if constexpr (EPI != kEpiPlain) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        g16_load_res<32>(args, args.res, tl.group, row, col_p + c * 32, col_end, valid, res[c]);
-        if constexpr (EPI == kEpiPoly) g16_load_res<32>(args, args.res_lo, tl.group, row, col_p + c * 32, col_end, valid, low[c]);
-      }
+      for (int c = 0; c < 2; ++c)
+        g16_load_res<32>(args, args.res, tl.group, row, col_w + c * 32, col_end, valid, res[c]);
     }
-    got = wait16<false>(acc_bar, 0, abort_flag, args.wait_ns);
+    const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+    // 32 columns of this thread's accumulator row (16 where a CTA has no more)
+    const int unit = width < 32 ? 16 : 32;
+    auto columns = [&](int col_t, bool whole, uint32_t (&raw)[32]) {
+      __syncwarp();  // TMEM loads are the whole warp's
+      if (whole) {
+        tc_ld_32x32b_x32(t_row + col_t, raw);
+      } else {
+        uint32_t r16[16];
+        tc_ld_32x32b_x16(t_row + col_t, r16);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          raw[j] = r16[j];
+          raw[16 + j] = 0;
+        }
+      }
+      tc_wait_ld();
+    };
+    // 32 columns of the warp's rows to global memory through a
+    // tile in shared memory, so that a store has 64 bytes each of eight rows (16 of
+    // each of 32 took 1 us of a tile's 5.7)
+    const uint32_t stg = sbase + L::OFF_STG + ew * L::STG_BYTES;
+    auto store = [&](void* out, const float (&v)[32], int col0) {
+      const int h = args.out_type == 1;
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* f = v + q * 8;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)),
+                     "r"(pack16(f[0], f[1], h)), "r"(pack16(f[2], f[3], h)), "r"(pack16(f[4], f[5], h)),
+                     "r"(pack16(f[6], f[7], h))
+                     : "memory");
+      }
+      __syncwarp();
+      const int q = lane & 3, col = col0 + q * 8;
+      uint16_t* to = static_cast<uint16_t*>(out) + tl.group * args.d_batch + col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2);
+        if (row_w + rr < tl.rows_end && col < col_end) {
+          uint4 w;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                       : "r"(stg + rr * 64 + ((q ^ ((rr >> 1) & 3)) << 4))
+                       : "memory");
+          *reinterpret_cast<uint4*>(to + (row_w + rr) * args.d_ld) = w;
+        }
+      }
+    };
+    bool got = wait16<false>(acc_bar, 0, abort_flag, args.wait_ns);
     got = __all_sync(0xFFFFFFFFu, got);
     if (!got && lane == 0) {
       report(args.status, 0x4);
       *abort_flag = 1;
     }
     tc_fence_after();
-  }
-  // 32 columns of this thread's accumulator row (16 where a CTA has no more)
-  auto columns = [&](int col_t, uint32_t (&raw)[32]) {
-    __syncwarp();  // TMEM loads are the whole warp's
-    if (width >= 32) {
-      tc_ld_32x32b_x32(t_row + col_t, raw);
-    } else {
-      uint32_t r16[16];
-      tc_ld_32x32b_x16(t_row + col_t, r16);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        raw[j] = r16[j];
-        raw[16 + j] = 0;
-      }
-    }
-    tc_wait_ld();
-  };
-  if (splits > 1) {
-    // every CTA's MMAs have read their operands: the rings can take partial sums
-    cluster_sync();
-    if (warp >= 2 && got && tl.row0 + quarter * 32 < tl.rows_end) {
-      for (int o = 1; o < splits; ++o) {
-        const int owner = (part + o) % splits;
-        const int slot = part < owner ? part : part - 1;
-        // [slot][quad of columns][row] of float4: a warp's 32 rows are 512 bytes
-        const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>((slot * (width / 4) * kS16T + r) * 16);
+    const bool rows_here = got && row_w < tl.rows_end;
+    if (splits > 1) {
+      // every CTA's MMAs have read their operands: the rings can take partial sums
+      cluster_sync();
+      if (rows_here) {
+        const int per = width / unit;  // units of an owner's columns, shared by the warps of a quarter
 #pragma unroll 1
-        for (int c = 0; c < width; c += 32) {
+        for (int u = grp; u < (splits - 1) * per; u += grps) {
+          const int o = 1 + u / per, c = (u % per) * unit;
+          const int owner = (part + o) % splits;
+          const int slot = part < owner ? part : part - 1;
+          // [slot][quad of columns][row] of float4: a warp's 32 rows are 512 bytes
+          const uint32_t dst = map_to_rank(sbase, owner) + static_cast<uint32_t>(((slot * width + c) / 4 * kS16T + r) * 16);
           uint32_t raw[32];
-          columns(owner * width + c, raw);
+          columns(owner * width + c, unit == 32, raw);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (c + j * 4 < width)
-              st_cluster_v4(dst + (c / 4 + j) * kS16T * 16, raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
+            if (j * 4 < unit)
+              st_cluster_v4(dst + j * kS16T * 16, raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
         }
       }
+      cluster_sync();
     }
-    cluster_sync();
-  }
-  if (warp >= 2 && got && tl.row0 + quarter * 32 < tl.rows_end) {
-    const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+#pragma unroll 1
+    for (int ci = 0; ci < 2 && rows_here; ++ci) {
+      const int c = wc + ci * 32;  // of the CTA's columns
+      const int col0 = col_w + ci * 32;
+      if (col0 >= col_end) break;
+      uint4 low[4];
+      if constexpr (EPI == kEpiPoly) g16_load_res<32>(args, args.res_lo, tl.group, row, col0, col_end, valid, low);
+      uint32_t raw[32];
+      columns(part * width + c, wcols >= 32, raw);
+      float v[32];
 #pragma unroll
-    for (int ci = 0; ci < 4; ++ci) {
-      const int c = ci * 32;
-      const int col0 = col_p + c;
-      if (c < width && col0 < args.n) {
-        uint32_t raw[32];
-        columns(part * width + c, raw);
-        float v[32];
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+#pragma unroll 1
+      for (int slot = 0; slot < splits - 1; ++slot) {
+        const float4* src = reinterpret_cast<const float4*>(smem) + (slot * width + c) / 4 * kS16T + r;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
-        for (int slot = 0; slot < splits - 1; ++slot) {
-          const float4* src = reinterpret_cast<const float4*>(smem) + ((slot * width + c) / 4) * kS16T + r;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (c + j * 4 < width) {
-              const float4 f = src[j * kS16T];
-              v[4 * j] += f.x;
-              v[4 * j + 1] += f.y;
-              v[4 * j + 2] += f.z;
-              v[4 * j + 3] += f.w;
-            }
+        for (int j = 0; j < 8; ++j) {
+          if (j * 4 < wcols) {
+            const float4 f = src[j * kS16T];
+            v[4 * j] += f.x;
+            v[4 * j + 1] += f.y;
+            v[4 * j + 2] += f.z;
+            v[4 * j + 3] += f.w;
           }
         }
-        g16_epilogue<EPI, 32>(args, v, res[ci], low[ci], bias + c, tl.group, row, col0, scale);
-        if constexpr (EPI == kEpiLinear) {
-          if (args.z != nullptr && valid) g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
-          g16_activate<32>(args, v, res[ci]);
+      }
+      g16_epilogue<EPI, 32>(args, v, res[0], low, bias + c, tl.group, row, col0, scale);
+      if constexpr (EPI == kEpiLinear) {
+        if (args.z != nullptr) store(args.z, v, col0);
+        g16_activate<32>(args, v, res[0]);
+      }
+      if constexpr (EPI == kEpiPoly) {
+        if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, col_end, valid);
+      }
+      store(args.d, v, col0);
+      if constexpr (EPI == kEpiPoly) {
+        if (args.z != nullptr) {
+          g16_remainder<32>(args, v);
+          store(args.z, v, col0);
         }
-        if constexpr (EPI == kEpiPoly) {
-          if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, col_end, valid);
-        }
-        if (valid) {
-          g16_store_row<32>(args, args.d, v, tl.group, row, col0, col_end);
-          if constexpr (EPI == kEpiPoly) {
-            if (args.z != nullptr) {
-              g16_remainder<32>(args, v);
-              g16_store_row<32>(args, args.z, v, tl.group, row, col0, col_end);
-            }
-          }
-        }
+      }
+      if constexpr (EPI != kEpiPlain) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) res[0][q] = res[1][q];
       }
     }
   }
@@ -903,7 +950,7 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
 }
 
 template <int EPI, int STAGES>
-__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
+__global__ void __launch_bounds__(s16_threads(1), STAGES <= 3 ? 2 : 1)
     g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ G16Args args) {
   g16_small_cta<EPI, STAGES>(&tmap_a, &tmap_b, args, static_cast<int>(blockIdx.x));
@@ -918,7 +965,7 @@ struct G16Two {
 };
 
 template <int STAGES>
-__global__ void __launch_bounds__(kS16Threads, STAGES <= 3 ? 2 : 1)
+__global__ void __launch_bounds__(s16_threads(1), STAGES <= 3 ? 2 : 1)
     g16_two_kernel(const __grid_constant__ CUtensorMap a1, const __grid_constant__ CUtensorMap b1,
                    const __grid_constant__ CUtensorMap a2, const __grid_constant__ CUtensorMap b2,
                    const __grid_constant__ G16Two two) {
@@ -1043,7 +1090,7 @@ static int64_t lone_clusters(int splits, int num_sms) {
     static std::atomic<bool> done[kMaxDevices];
     if (allow_smem(g16_small_kernel<kEpiPlain, 6>, S16Layout<6>::ALLOC, done) != cudaSuccess) return 0;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = g16_config(splits, kS16Threads, S16Layout<6>::ALLOC, splits, nullptr, attr);
+    cudaLaunchConfig_t cfg = g16_config(splits, s16_threads(splits), S16Layout<6>::ALLOC, splits, nullptr, attr);
     cfg.numAttrs = 1;
     if (cudaOccupancyMaxActiveClusters(&v, g16_small_kernel<kEpiPlain, 6>, &cfg) != cudaSuccess || v <= 0) {
       cudaGetLastError();
@@ -1062,7 +1109,7 @@ static cudaError_t launch_small16s(const CUtensorMap& ta, const CUtensorMap& tb,
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
-      g16_config(tiles * a.splits, kS16Threads, S16Layout<STAGES>::ALLOC, a.splits, stream, attr);
+      g16_config(tiles * a.splits, s16_threads(a.splits), S16Layout<STAGES>::ALLOC, a.splits, stream, attr);
   return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI, STAGES>, ta, tb, a);
 }
 
@@ -1282,7 +1329,7 @@ cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cud
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
-      g16_config((t1 + t2) * s, kS16Threads, lone ? S16Layout<6>::ALLOC : S16Layout<3>::ALLOC, s, stream, attr);
+      g16_config((t1 + t2) * s, s16_threads(s), lone ? S16Layout<6>::ALLOC : S16Layout<3>::ALLOC, s, stream, attr);
   return lone ? cudaLaunchKernelEx(&cfg, g16_two_kernel<6>, a1, b1, a2, b2, two)
               : cudaLaunchKernelEx(&cfg, g16_two_kernel<3>, a1, b1, a2, b2, two);
 }
