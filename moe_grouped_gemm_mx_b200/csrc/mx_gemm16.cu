@@ -1124,16 +1124,16 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, and how many CTAs share a tile's K: the one whose estimated time
 // (in us, fitted to measured launches) is less.
-//   pair kernel: 8 us for launch, first operands and last epilogue, and 0.3 us per
-//     K chunk of 64 for each round of tiles (4096x1024x1024 12.8 us estimated, 12.9
-//     measured; 1037x7168x2048 27.2, 28.4; 64x2112x7168 42, 38.5).
-//   small kernel: 4 us, the exchange of partial sums, and per K chunk of a CTA
-//     0.25 us where it has an SM to itself (six stages), 0.39 us with three stages,
-//     0.51 us where two share one (and 1.5 us to start); the first six chunks
-//     0.15 us more each, and
-//     2.5 us for every further round, and its epilogue, shared by a split
-//     (64x2112x7168 by 4: 13.2 estimated, 12.9 measured; by 2: 20, 19.7;
-//     1037x7168x2048 whole: 43, 38.7).
+//   pair kernel: 7 us for launch, first operands and last epilogue, and 0.31 us per
+//     K chunk of 64 for each round of tiles (1024x1024x1024 12 us estimated, 11.4
+//     measured; 1037x7168x2048 26.8, 28.1; 64x2112x7168 41.7, 38.5).
+//   small kernel: 3.6 us with a plain epilogue, the exchange of partial sums, and per
+//     K chunk of a CTA 0.27 us where all clusters have SMs to themselves (six stages);
+//     else 2.6 us more, 0.3 us a chunk, or 0.4 us where there are more CTAs than SMs, and
+//     2.5 us for every further round (256x256x256 whole: 4.7 estimated, 4.8 measured;
+//     64x2112x7168 by 4: 13.2, 12.6; by 2: 20.4, 18.7; 128x4224x4096 by 4, 33 clusters
+//     that fit: 9.9, 11.1; 128x4352x4096, 34 that do not: 13.0, 12.9; 1037x7168x2048
+//     whole: 34.3, 34.2).
 struct G16Tiles {
   double pair, small;  // 256 x 256 and 128 x 128 tiles to do
   int64_t chunks;      // of 64 of K
@@ -1157,13 +1157,15 @@ static G16Tiles count_tiles(const Gemm16& p) {
   return c;
 }
 
-static double pair_cost(const G16Tiles& c, int num_sms) {
-  return 8.0 + 0.3 * std::ceil(c.pair / (num_sms / 2)) * static_cast<double>(c.chunks);
+// What an epilogue adds to the last tile, in us.
+static double epilogue_cost(const Gemm16& p) {
+  if (p.epi == kEpiPoly) return 3.5;
+  return p.epi == kEpiLinear ? (p.act != 0 ? 1.8 : 0.8) : 0.0;
 }
 
-// The small kernel's epilogue on a whole tile, in us: C, the mirrored tile and a low
-// half make it longest.
-static double epilogue_cost(const Gemm16& p) { return p.epi == kEpiPoly ? 1.6 : p.epi == kEpiLinear ? 1.0 : 0.5; }
+static double pair_cost(const G16Tiles& c, double epilogue, int num_sms) {
+  return 7.0 + epilogue + 0.31 * std::ceil(c.pair / (num_sms / 2)) * static_cast<double>(c.chunks);
+}
 
 // The small kernel's cost on `tiles` tiles, the longest of `chunks`, and the best
 // split, at most one CTA per chunk of the product with the fewest.
@@ -1173,13 +1175,13 @@ static double small_cost(double tiles, int64_t chunks, int64_t fewest, double ep
   for (int s = 1; s <= 8; s *= 2) {
     if (s > fewest || (s > 1 && tiles * s > 2.0 * num_sms)) break;
     const double each = static_cast<double>(ceil_div(chunks, s));
-    const double exchange = s == 1 ? 0.0 : s == 2 ? 0.6 : s == 4 ? 1.0 : 1.3 + 0.2 * tiles;
+    const double exchange = s == 1 ? 0.0 : s == 2 ? 1.65 : s == 4 ? 2.0 : 3.0;
     const double rounds = std::ceil(tiles * s / (2.0 * num_sms));
-    double cost = 4.0 + exchange + 0.15 * std::fmin(each, 6.0) + epilogue / s;
+    double cost = 3.6 + exchange + (s == 1 ? epilogue : 0.5 * epilogue);  // a warp has 64 columns, else 32 or less
     if (tiles <= static_cast<double>(lone_clusters(s, num_sms)))
-      cost += 0.25 * each;
+      cost += 0.27 * each;
     else
-      cost += (tiles * s <= num_sms ? 0.39 * each : 1.5 + 0.51 * each * rounds) + 2.5 * (rounds - 1.0);
+      cost += 2.6 + (tiles * s <= num_sms ? 0.3 * each : 0.4 * each * rounds) + 2.5 * (rounds - 1.0);
     if (cost < best) {
       best = cost;
       *splits = s;
@@ -1218,7 +1220,7 @@ static G16Choice choose(const Gemm16& p, int num_sms) {
   }
   if (!small_can(p)) return c;
   const G16Tiles tiles = count_tiles(p);
-  c.small = small_cost(tiles.small, tiles.chunks, tiles.chunks, epilogue_cost(p), num_sms, &c.splits) < pair_cost(tiles, num_sms);
+  c.small = small_cost(tiles.small, tiles.chunks, tiles.chunks, epilogue_cost(p), num_sms, &c.splits) < pair_cost(tiles, epilogue_cost(p), num_sms);
   return c;
 }
 
@@ -1305,8 +1307,8 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
 cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cudaStream_t stream) {
   const G16Tiles tp = count_tiles(p), tq = count_tiles(q);
   int sp = 1, sq = 1, s = 1;
-  const double apart = std::fmin(small_cost(tp.small, tp.chunks, tp.chunks, epilogue_cost(p), num_sms, &sp), pair_cost(tp, num_sms)) +
-                       std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, epilogue_cost(q), num_sms, &sq), pair_cost(tq, num_sms));
+  const double apart = std::fmin(small_cost(tp.small, tp.chunks, tp.chunks, epilogue_cost(p), num_sms, &sp), pair_cost(tp, epilogue_cost(p), num_sms)) +
+                       std::fmin(small_cost(tq.small, tq.chunks, tq.chunks, epilogue_cost(q), num_sms, &sq), pair_cost(tq, epilogue_cost(q), num_sms));
   const int64_t longest = tp.chunks > tq.chunks ? tp.chunks : tq.chunks, fewest = tp.chunks < tq.chunks ? tp.chunks : tq.chunks;
   const bool together = p.mode == kBatched && q.mode == kBatched && p.epi == kEpiPlain && q.epi == kEpiPlain && small_can(p) &&
                         small_can(q) && forced_config() < 0 &&
