@@ -489,26 +489,19 @@ __device__ __forceinline__ void g16_remainder(const G16Args& a, float (&v)[C]) {
   }
 }
 
-// C columns of one row to global memory, whole groups of 8 columns before `end`
-// (rows are padded to a multiple of 8 elements).
+// C columns of one row to global memory (16-bit), whole groups of 8 columns before
+// `end` (rows are padded to a multiple of 8 elements).
 template <int C>
 __device__ __forceinline__ void g16_store_row(const G16Args& a, void* out, const float (&v)[C], int group, int64_t row,
                                               int col0, int end) {
-  const int64_t at = group * a.d_batch + row * a.d_ld + col0;
+  uint16_t* to = static_cast<uint16_t*>(out) + group * a.d_batch + row * a.d_ld + col0;
+  const int h = a.out_type == 1;
 #pragma unroll
   for (int g = 0; g < C / 8; ++g) {
-    if (col0 + g * 8 < end) {
-      const float* p = v + g * 8;
-      if (a.out_type == 2) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at + g * 8);
-        o[0] = make_float4(p[0], p[1], p[2], p[3]);
-        o[1] = make_float4(p[4], p[5], p[6], p[7]);
-      } else {
-        const int h = a.out_type == 1;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + g * 8) =
-            make_uint4(pack16(p[0], p[1], h), pack16(p[2], p[3], h), pack16(p[4], p[5], h), pack16(p[6], p[7], h));
-      }
-    }
+    const float* p = v + g * 8;
+    if (col0 + g * 8 < end)
+      *reinterpret_cast<uint4*>(to + g * 8) =
+          make_uint4(pack16(p[0], p[1], h), pack16(p[2], p[3], h), pack16(p[4], p[5], h), pack16(p[6], p[7], h));
   }
 }
 

@@ -18,6 +18,11 @@
 // operand of X X^T and an MN-major one of B X.  A tall matrix is read and written
 // transposed.  One CTA to an SM: the launch asks for all shared memory, since CTAs
 // of two clusters that waited for each other's TMEM on two SMs would never finish.
+//
+// Bound by latency, not by bytes or products (0.14 us): 32 x 7168 takes 37 us in 16
+// CTAs, 12 for launch, read, norm and result and 5 a step (three products, two
+// cluster barriers, two exchanges); the general path takes 102.  (With 256 threads
+// and loads of single elements it was 63.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
