@@ -20,10 +20,11 @@
 // large singular values, where its rounding is not multiplied.  A, B: one FP16 number.
 //
 // Bound by the tensor cores: five steps of 8 x 4096 x 7168 are 17.2 TFLOP and take
-// 14.4 ms (1195 TFLOP/s; the diagonal tiles' lower halves, 6 % of A's and B's, are
-// computed too), of which the sum of squares and the start are 0.2.  A 256 x 256
-// matrix takes 106 us, 6 us for each of 17 launches.  (Reading an FP32 G of 4 x 7168
-// x 2048 by 16 bytes instead of 4 took the start from 134 to 78 us.)
+// 12.9 ms on a card that has rested (1330 TFLOP/s), 15.3 in loops at its power limit,
+// of which the sum of squares and the start are 0.2.  The diagonal tiles' lower
+// halves, 6 % of A's and B's, are computed too.  A 256 x 256 matrix takes 106 us, 6 us
+// for each of 17 launches.  (Reading an FP32 G of 4 x 7168 x 2048 by 16 bytes instead
+// of 4 took the start from 134 to 78 us.)
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
