@@ -136,6 +136,18 @@ def test_forward_in_place_residual(mx):
             assert got is r and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("cfg", [1, 2, 8])
+@pytest.mark.parametrize("shape", [(129, 136, 264), (333, 520, 520)], ids=lambda s: "x".join(map(str, s)))
+def test_forward_in_place_residual_by_tile(mx, cfg, shape):
+    """The same where other lanes store than those that read the residual."""
+    m, n, k = shape
+    with config(cfg):
+        x, w, r = normal((m, k), FP16, 1), normal((n, k), FP16, 2, 0.06), normal((m, n), FP16, 3)
+        want = mx.mx_linear_act(x, w, residual=r, activation="gelu")
+        got = mx.mx_linear_act(x, w, residual=r, activation="gelu", y=r)
+        assert got is r and torch.equal(got, want)
+
+
 def test_results_do_not_vary(mx):
     """The same call gives the same bits (split sums meet in a fixed order)."""
     for cfg in (0, 8):
