@@ -941,10 +941,8 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
             dbias = dy.new_empty(n)
         if act != 0 and dz is None:
             dz = torch.empty_like(dy)
-        if dbias is not None and workspace is None and m > 0 and n > 0:
-            need = mx_linear_act_backward_workspace_bytes(m, n)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if dbias is not None and workspace is None and m > 1024:  # up to there none is needed
+            workspace = torch.empty(mx_linear_act_backward_workspace_bytes(m, n), dtype=torch.uint8, device=dev)
         _raise(_lib.mx_linear_act_backward(_ptr(dy), _ptr(z), _ptr(x), _ptr(w), _ptr(dz), _ptr(dx), _ptr(dw),
                                            _ptr(dbias), m, n, k, _DTYPES[dt], act, _ptr(workspace),
                                            0 if workspace is None else workspace.numel(),
