@@ -583,13 +583,42 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
               g16_epilogue<EPI, 32>(args, v, res, low, nullptr, tl.group, row, col_w + c, scale);
               if (args.sym && tl.mb != tl.nb)
                 g16_store_mirror<32>(args, v, tl.group, row, col_w + c, args.n, valid);
+              if (args.z != nullptr) {
+                // the low half of D, through the staging tile before D itself: a store has
+                // 64 bytes each of eight rows (16 of each of 32: 4 x 1536 x 1536 428 us, so 415)
+                uint4 l[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t u[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float a0 = v[8 * q + 2 * j], a1 = v[8 * q + 2 * j + 1];
+                    const float2 r2 = unpack16(pack16(a0, a1, 1), 1);
+                    u[j] = pack16(a0 - r2.x, a1 - r2.y, 1);
+                  }
+                  l[q] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                stage32(c, l);
+                __syncwarp();
+                const int col = col_w + c + (lane & 3) * 8;
+                uint16_t* to = static_cast<uint16_t*>(args.z) + tl.group * args.d_batch + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int rr = i * 8 + (lane >> 2);
+                  if (row_w + rr < tl.rows_end && col < args.n) {
+                    uint4 q;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                 : "r"(stg + rr * 128 + (((c / 8 + (lane & 3)) ^ (rr & 7)) << 4))
+                                 : "memory");
+                    *reinterpret_cast<uint4*>(to + (row_w + rr) * args.d_ld) = q;
+                  }
+                }
+                __syncwarp();
+              }
               uint4 w[4];
               pack32(v, w);
               stage32(c, w);
-              if (args.z != nullptr && valid) {  // the low half of D, past the staging tile
-                g16_remainder<32>(args, v);
-                g16_store_row<32>(args, args.z, v, tl.group, row, col_w + c, args.n);
-              }
             } else if (c == 32) {
               release();
             }
