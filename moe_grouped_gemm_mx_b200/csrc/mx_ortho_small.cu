@@ -157,17 +157,20 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const uint32_t as = xs + chunks * rp * 128;                        // A
   const uint32_t bs = as + (rp + 63) / 64 * rp * 128;                // B
   const uint32_t recv = bs + (rp + 63) / 64 * rp * 128;              // [source][column][row] partial sums
-  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8, factors 3 x 4
+  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8, factors 3 x 4, failed 4, drain barrier 8
   const uint32_t bar = misc;
   auto at = [&](uint32_t addr) { return smem + (addr - sbase); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(at(misc + 8));
   double* block_sums = reinterpret_cast<double*>(at(misc + 16));
   const uint32_t cluster_sums = misc + 144;
   volatile float* factors = reinterpret_cast<volatile float*>(at(misc + 272));
+  const uint32_t failed = misc + 284, drain_bar = misc + 288;
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(drain_bar, 1);
     fence_mbar_init();
+    *reinterpret_cast<volatile uint32_t*>(at(failed)) = 0;
   }
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -181,10 +184,15 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const uint32_t t_a = slice;                     // TMEM column of A's partial sum and of A^2
+  // A wait that runs out (ok is the warp's) ends the warp's work: no wait, product or
+  // result after it, only the barriers that others are waiting at.  All learn of it
+  // at the next step's first cluster barrier and leave the steps there together.
+  // (Warp 0 issues all products, each after its own wait for the one before.)
   uint32_t parity = 0;
   bool ok = true;
   auto wait_mma = [&]() {
-    if (!wait16<false>(bar, parity, nullptr, args.wait_ns)) ok = false;
+    if (!ok) return;
+    ok = __all_sync(0xFFFFFFFFu, wait16<false>(bar, parity, nullptr, args.wait_ns));
     parity ^= 1u;
     tc_fence_after();
   };
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ok && elect_one()) {
       tc_fence_after();
       const int live = c - c0 < slice ? (c - c0 > 0 ? (c - c0 + 63) / 64 : 1) : chunks;  // the others are zeros
       uint64_t d = desc_kmajor_sw128(xs);
@@ -341,7 +349,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // instead, as the general form does: nothing multiplies X's rounding any more,
     // and a X of one X with B X of another would only add the difference.
     const bool add_x = step == 0 || step + 2 < args.steps;
-    for (int j = add_x ? first : chunks; j < chunks; j += kNsGroups) {
+    for (int j = add_x && ok ? first : chunks; j < chunks; j += kNsGroups) {
       uint32_t v[2][32];
       load_x(j, v[0], v[1]);
 #pragma unroll
@@ -353,8 +361,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     }
     tc_wait_st();
     wait_mma();
+    if (!ok && lane < cs) st_cluster_b32(map_to_rank(failed, lane), 1u);
     // ---- partial sums to the CTAs that add them
-    for (int b = first16; b < rp / 16; b += kNsGroups) {
+    for (int b = ok ? first16 : rp / 16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
       __syncwarp();
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
@@ -374,6 +383,11 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
       }
     }
     cluster_sync();
+    // (nobody writes here before all have passed the next barrier: the cluster agrees)
+    if (*reinterpret_cast<volatile uint32_t*>(at(failed)) != 0) {
+      ok = false;
+      break;
+    }
     // ---- added in rank order, and A 2^12 as FP16 to everyone.  Entry (row, col) is
     // stored as (col, row): the rows of a warp are then consecutive.
     if (row < rp) {
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     // leaves in A's place (A^2 is done, each entry of A is read by the lane that
     // writes there): near the fixed point a and B cancel to a fifth, and B's rounding
     // was half the method's error
-    for (int b = first16; b < rp / 16; b += kNsGroups) {
+    for (int b = ok ? first16 : rp / 16; b < rp / 16; b += kNsGroups) {
       uint32_t v[16];
       __syncwarp();
       tc_ld_32x32b_x16(t_row + t_a + b * 16, v);
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     // ---- a X + B X, up to 256 columns an instruction
-    if (warp == 0 && elect_one()) {
+    if (warp == 0 && ok && elect_one()) {
       tc_fence_after();
       for (int n0 = 0; n0 < slice; n0 += 256) {
         const uint32_t idesc = idesc_f16(128, slice - n0 < 256 ? slice - n0 : 256, 1, 0, 1);
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     __syncwarp();
     wait_mma();
     if (step + 1 < args.steps) {
-      for (int j = first; j < chunks; j += kNsGroups) {
+      for (int j = ok ? first : chunks; j < chunks; j += kNsGroups) {
         uint32_t v[2][32];
         load_x(j, v[0], v[1]);
         put_x(j, 0, v[0]);
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   // ---- out
   const float last = inv_sa * scalbnf(1.0f, -args.log_sx);
   __nv_bfloat16* out = args.out + static_cast<int64_t>(batch) * args.m * args.n;
-  for (int j = first; j < chunks; j += kNsGroups) {
+  for (int j = ok ? first : chunks; j < chunks; j += kNsGroups) {
     const int col = c0 + j * 64;
     uint32_t v[2][32], o[32];  // o: pairs of columns
     load_x(j, v[0], v[1]);
@@ -505,6 +519,12 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     }
   }
   if (!ok && lane == 0) report(args.status, 0x4);
+  // products still under way end before their operands and accumulators are given up
+  if (warp == 0 && !ok && elect_one()) {
+    tc_commit(drain_bar);
+    wait16<false>(drain_bar, 0, nullptr, 100000000ull);
+  }
+  __syncwarp();
   // no CTA leaves while another may still write into its shared memory
   tc_fence_before();
   cluster_sync();
