@@ -469,7 +469,10 @@ mx_status mx_moe_combine_peer(const void *const *y_peers, int32_t ranks, int64_t
  * around the experts, experts held in 16 bits, and the optimiser's update of
  * their weights (the pages quantise the expert GEMMs; "DeepSeek drops DeepGEMM"
  * page, FP8 mixed precision: sensitive parts stay in BF16).  Operands are BF16
- * or FP16, row-major, 16-byte aligned; sums are FP32; results are rounded once.
+ * or FP16, row-major, 16-byte aligned; results are rounded once.  Sums are FP32:
+ * of at most 2^14 terms in the tensor core's accumulator, which truncates (numbers
+ * of one sign lose up to 1e-4 there), longer ones as rounded sums of parts of 2^13;
+ * FP32 results in parts of 512.
  * Row lengths that a tensor map must describe are multiples of 8 elements.
  * Sizes are at most 2^31 - 1024, and what a product sums over at most 2^27.
  */

@@ -18,6 +18,10 @@
 //    with GELU and the pre-activation the tensor pipe is active 82 % of the time.
 //    Where K is short the epilogue bounds it: 16384x4096x256 46 us plain, 52 with bias,
 //    80 with bias and GELU, 81 with bias and residual.
+//    Sums longer than an accumulator may take (kSumWhole) have a form of their own
+//    (kEpiLong; the small kernel's LONG), which adds the parts in registers (there: in
+//    TMEM): 2048x2048x32768 182 us against 181 in one accumulator, 64x2112x65536 64 against
+//    63, the 16-bit weight gradient of 65536 rows over 32 experts (7168x2048) equal.
 //
 //  g16_small_kernel  one CTA per 128 x 128 tile, K split over a cluster of 1, 2,
 //    4 or 8 CTAs whose partial sums meet in distributed shared memory (in a
@@ -50,7 +54,10 @@ __host__ __device__ constexpr int p16_threads(int epi) {
 }
 constexpr int kP16TM = 256, kP16TN = 256;
 constexpr int kP16K = 64;     // elements of K per stage
-constexpr int kP16Seg = 512;  // kEpiSum: K per partial sum
+// K of one accumulator (FP32 results show what it truncates long before 16-bit ones do)
+__host__ __device__ constexpr int p16_part(int epi, int kn) {
+  return epi == kEpiSum ? 512 : epi == kEpiLong && kn > kSumWhole ? kSumPart : kn;
+}
 
 // 16 epilogue warps take a stage's place for their staging tiles, where the
 // residual's (or C's) rows wait for the sum (five stages cost about 1 % of a long
@@ -205,7 +212,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
       // ===== MMA issuer: up to 4 pair MMAs of K = 16 per stage.  Accumulator
-      // buffer `it & 1` takes a tile's sum, or (kEpiSum) that of kP16Seg of its K.
+      // buffer `it & 1` takes a tile's sum, or (kEpiSum, kEpiLong) that of a part of its K.
       const uint32_t idesc = idesc_f16(kP16TM, kP16TN, args.op_fp16, args.a_mn, args.b_mn);
       const uint64_t da0 = args.a_mn ? desc_mnmajor_sw128(sbase + L::OFF_A, 8192) : desc_kmajor_sw128(sbase + L::OFF_A);
       const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
@@ -224,7 +231,8 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
           if (!wait16<true>(acce_bar(buf), ((it >> 1) & 1u) ^ 1u, abort_flag, args.wait_ns)) { ok = false; break; }
           tc_fence_after();
           const uint32_t acc = tmem_base + buf * kP16TN;
-          const int k_end = EPI == kEpiSum && kn - kk > kP16Seg ? kk + kP16Seg : kn;
+          const int part = p16_part(EPI, kn);
+          const int k_end = kn - kk > part ? kk + part : kn;
           uint32_t accumulate = 0;
           for (; kk < k_end; kk += kP16K) {
             if (needs_clearing(kn - kk)) {
@@ -334,7 +342,8 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
     };
     // the accumulator's next buffer is full; false (on every lane) if the wait ran out
     auto wait_full = [&]() -> bool {
-      const bool got = wait16<false>(accf_bar(it & 1u), (it >> 1) & 1u, abort_flag, args.wait_ns);
+      // (a part of a long sum is there before 32 attempts have failed)
+      const bool got = wait16<false, EPI == kEpiLong ? 2 : 32>(accf_bar(it & 1u), (it >> 1) & 1u, abort_flag, args.wait_ns);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         if (lane == 0) {
           report(args.status, 0x4);
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
       const bool tma = args.mode != kRaggedM || row_w + 32 <= tl.rows_end;
       const int z_out = args.mode == kRaggedM ? 0 : tl.group;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * WCOLS;
-      if constexpr (EPI == kEpiPlain || EPI == kEpiSum) {
+      if constexpr (EPI == kEpiPlain || EPI == kEpiSum || EPI == kEpiLong) {
         if (kn == 0) {  // a group without tokens: zeros from the staging tile, no accumulator
           if (mine) {
             if (!zeros) {
@@ -389,35 +398,8 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
         }
         zeros = false;
       }
-      if constexpr (EPI == kEpiSum) {
-        // FP32 sums over a long K: the tensor core's accumulator truncates, so each
-        // kP16Seg of K goes into one of its own, and these are added here, rounded
-        float sum[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-        for (int kk = 0; kk < kn; kk += kP16Seg) {
-          ok = wait_full();
-          if (!ok) break;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t raw[16];
-            tc_ld_32x32b_x16(t_row + (it & 1u) * kP16TN + c * 16, raw);
-            tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(raw[j]);
-          }
-          release();
-        }
-        if (!ok) break;
-        if (mine) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (col_w + c * 32 < args.n)
-              put(&tmap_d, reinterpret_cast<const uint32_t*>(sum) + c * 32, col_w + c * 32, row_w, z_out);
-        }
-      } else if constexpr (EPI == kEpiPlain) {
-        ok = wait_full();
-        if (!ok) break;
+      // one accumulator has the whole sum: 64 columns at a time
+      auto plain = [&]() {
 #pragma unroll 1
         for (int c = 0; c < 128; c += 64) {
           const int col0 = col_w + c;
@@ -445,6 +427,95 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
             g16_store_row<64>(args, args.d, v, tl.group, row, col0, args.n);
           }
         }
+      };
+      const int part = p16_part(EPI, kn);
+      if (EPI == kEpiLong && part >= kn && args.epi == kEpiPlain) {  // a short group among long ones
+        ok = wait_full();
+        if (!ok) break;
+        plain();
+        continue;
+      }
+      if constexpr (EPI == kEpiSum || EPI == kEpiLong) {
+        // long sums: the tensor core's accumulator truncates, so each part of K goes
+        // into one of its own, and these are added here, rounded
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        for (int kk = 0; kk < kn; kk += part) {
+          ok = wait_full();
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t raw[16];
+            tc_ld_32x32b_x16(t_row + (it & 1u) * kP16TN + c * 16, raw);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(raw[j]);
+          }
+          release();
+        }
+        if (!ok) break;
+        if constexpr (EPI == kEpiSum) {
+          if (mine) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (col_w + c * 32 < args.n)
+                put(&tmap_d, reinterpret_cast<const uint32_t*>(sum) + c * 32, col_w + c * 32, row_w, z_out);
+          }
+        } else if (mine && args.epi == kEpiPlain && tma) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 64) {
+            if (col_w + c < args.n) {
+              uint32_t w[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = pack16(sum[c + 2 * j], sum[c + 2 * j + 1], h);
+              put(&tmap_d, w, col_w + c, row_w, z_out);
+            }
+          }
+        } else if (mine) {
+          // the other epilogues, 32 columns at a time by plain loads and stores: next to
+          // a long sum they are nothing
+          const float scale = args.epi == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            const int col0 = col_w + c;
+            if (col0 < args.n) {
+              float v[32];
+              uint4 res[4], low[4];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = sum[c + j];
+              g16_load_res<32>(args, args.res, tl.group, row, col0, args.n, valid, res);
+              if (args.epi == kEpiLinear) {
+                if (args.bias != nullptr) {
+                  uint32_t bias2 = 0;
+                  if (lane < 16 && col0 + 2 * lane < args.n)
+                    bias2 = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(args.bias) + col0) + lane);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    const float2 b = unpack16(__shfl_sync(0xFFFFFFFFu, bias2, j), args.op_fp16);
+                    v[2 * j] += b.x;
+                    v[2 * j + 1] += b.y;
+                  }
+                }
+                if (args.z != nullptr && valid) g16_store_row<32>(args, args.z, v, tl.group, row, col0, args.n);
+                g16_activate<32>(args, v, res);
+              } else if (args.epi == kEpiPoly) {
+                g16_load_res<32>(args, args.res_lo, tl.group, row, col0, args.n, valid, low);
+                g16_epilogue<kEpiPoly, 32>(args, v, res, low, nullptr, tl.group, row, col0, scale);
+                if (args.sym && tl.mb != tl.nb) g16_store_mirror<32>(args, v, tl.group, row, col0, args.n, valid);
+              }
+              if (valid) g16_store_row<32>(args, args.d, v, tl.group, row, col0, args.n);
+              if (args.epi == kEpiPoly && args.z != nullptr && valid) {
+                g16_remainder<32>(args, v);
+                g16_store_row<32>(args, args.z, v, tl.group, row, col0, args.n);
+              }
+            }
+          }
+        }
+      } else if constexpr (EPI == kEpiPlain) {
+        ok = wait_full();
+        if (!ok) break;
+        plain();
       } else {
         // 64 columns a warp, 32 at a time.  The rows of the residual or C come into the
         // staging tile by TMA, while the MMAs run if they can, and the result takes
@@ -662,7 +733,7 @@ struct S16Layout {
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + STAGES * OP_BYTES;
   static constexpr int OFF_BAR = OFF_B + STAGES * OP_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 3;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_TAB = (OFF_MISC + 16 + 15) / 16 * 16;
   static constexpr int OFF_BIAS = (OFF_TAB + (kMaxGroups / kTabStep + 1) * 4 + 15) / 16 * 16;
@@ -674,8 +745,11 @@ struct S16Layout {
   static_assert((STAGES <= 3 ? 2 : 1) * ALLOC <= 232448, "shared memory budget");
 };
 
-// One CTA's part of a product: `cta` counts from the product's first CTA.
-template <int EPI, int STAGES>
+// One CTA's part of a product: `cta` counts from the product's first CTA.  LONG: its
+// sum goes through the accumulator in parts of kSumPart, which the epilogue's warps
+// add up in TMEM columns behind it (64x2112x65536: 2 % of the time).  With three stages,
+// and so 96 registers, it spills 84 to 260 bytes, outside the loop over K.
+template <int EPI, int STAGES, bool LONG>
 __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const CUtensorMap* tmap_b, const G16Args& args,
                                               const int cta) {
   using L = S16Layout<STAGES>;
@@ -697,6 +771,9 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
   auto full_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * s; };
   auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
   const uint32_t acc_bar = sbase + L::OFF_BAR + 8u * (2 * S);
+  const uint32_t added_bar = acc_bar + 8, drain_bar = acc_bar + 16;  // LONG
+  constexpr int kTmem = LONG ? 2 * kS16T : kS16T;
+  constexpr int kPart = kSumPart / kS16K;  // chunks of an accumulator
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -704,6 +781,10 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(acc_bar, 1);
+    if constexpr (LONG) {
+      mbar_init(added_bar, (s16_threads(splits) - 64) / 32);  // one lane of each epilogue warp
+      mbar_init(drain_bar, 1);
+    }
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -727,7 +808,7 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
   if (tile >= total) return;  // the whole cluster has this tile (the grid covers the most tiles there can be)
 
   if (warp == 1) {
-    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kS16T);
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -789,10 +870,18 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
       const uint64_t db0 = args.b_mn ? desc_mnmajor_sw128(sbase + L::OFF_B, 8192) : desc_kmajor_sw128(sbase + L::OFF_B);
       const uint64_t da_step = args.a_mn ? 128 : 2, db_step = args.b_mn ? 128 : 2;  // 16 of K, in 16-byte units
       int s = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, added = 0;
       bool ok = true;
       for (int c = c_begin; c < c_end; ++c) {
-        const int i = c - c_begin;
+        const int i = LONG ? (c - c_begin) % kPart : c - c_begin;
+        if constexpr (LONG) {
+          if (i == 0 && c != c_begin) {  // the accumulator starts anew
+            tc_commit(acc_bar);
+            if (!wait16<false>(added_bar, added, abort_flag, args.wait_ns)) { ok = false; break; }
+            added ^= 1u;
+            tc_fence_after();
+          }
+        }
         if (!wait16<false>(full_bar(s), phase, abort_flag, args.wait_ns)) { ok = false; break; }
         const uint64_t da = da0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
         const uint64_t db = db0 + static_cast<uint64_t>(s * (L::OP_BYTES >> 4));
@@ -813,8 +902,10 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
         report(args.status, 0x4);
         *abort_flag = 1;
       }
-      tc_commit(acc_bar);  // on every path, so that nothing is in flight when TMEM is freed
-      wait16<false>(acc_bar, 0, nullptr, 100000000ull);
+      tc_commit(acc_bar);
+      // on every path, so that nothing is in flight when TMEM is freed
+      if constexpr (LONG) tc_commit(drain_bar);
+      wait16<false>(LONG ? drain_bar : acc_bar, 0, nullptr, 100000000ull);
     }
     __syncwarp();
   }
@@ -853,15 +944,16 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
         g16_load_res<32>(args, args.res, tl.group, row, col_w + c * 32, col_end, valid, res[c]);
     }
     const float scale = EPI == kEpiPoly ? g16_scale(args, tl.group) : 1.0f;
-    // 32 columns of this thread's accumulator row (16 where a CTA has no more)
+    // 32 columns of this thread's row of the sum (16 where a CTA has no more)
+    const uint32_t t_sum = LONG ? t_row + kS16T : t_row;
     const int unit = width < 32 ? 16 : 32;
     auto columns = [&](int col_t, bool whole, uint32_t (&raw)[32]) {
       __syncwarp();  // TMEM loads are the whole warp's
       if (whole) {
-        tc_ld_32x32b_x32(t_row + col_t, raw);
+        tc_ld_32x32b_x32(t_sum + col_t, raw);
       } else {
         uint32_t r16[16];
-        tc_ld_32x32b_x16(t_row + col_t, r16);
+        tc_ld_32x32b_x16(t_sum + col_t, r16);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           raw[j] = r16[j];
@@ -901,13 +993,41 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
         }
       }
     };
-    bool got = wait16<false>(acc_bar, 0, abort_flag, args.wait_ns);
-    got = __all_sync(0xFFFFFFFFu, got);
-    if (!got && lane == 0) {
-      report(args.status, 0x4);
-      *abort_flag = 1;
+    const int parts = LONG ? (c_end - c_begin + kPart - 1) / kPart : 1;
+    bool got = true;
+    for (int p = 0; p < parts && got; ++p) {
+      got = wait16<false, LONG ? 2 : 32>(acc_bar, p & 1, abort_flag, args.wait_ns);
+      got = __all_sync(0xFFFFFFFFu, got);
+      if (!got && lane == 0) {
+        report(args.status, 0x4);
+        *abort_flag = 1;
+      }
+      tc_fence_after();
+      if constexpr (LONG) {
+        const int span = kS16T / grps;  // columns that this warp adds
+        for (int c = grp * span; c < (grp + 1) * span && got; c += 32) {
+          uint32_t acc[32], sum[32];
+          __syncwarp();
+          tc_ld_32x32b_x32(t_row + c, acc);
+          if (p != 0) {
+            tc_ld_32x32b_x32(t_sum + c, sum);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] = __float_as_uint(__uint_as_float(acc[j]) + __uint_as_float(sum[j]));
+          }
+          tc_wait_ld();
+          tc_st_32x32b_x32(t_sum + c, acc);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (got && lane == 0 && p + 1 < parts) mbar_arrive(added_bar);
+      }
     }
-    tc_fence_after();
+    if constexpr (LONG) {  // a row's warps read what the others have added
+      named_barrier_sync(1, s16_threads(splits) - 64);
+      tc_fence_after();
+    }
     const bool rows_here = got && row_w < tl.rows_end;
     if (splits > 1) {
       // every CTA's MMAs have read their operands: the rings can take partial sums
@@ -984,15 +1104,15 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kS16T);
+    tmem_dealloc(tmem_base, kTmem);
   }
 }
 
-template <int EPI, int STAGES>
+template <int EPI, int STAGES, bool LONG>
 __global__ void __launch_bounds__(s16_threads(1), STAGES <= 3 ? 2 : 1)
     g16_small_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                      const __grid_constant__ G16Args args) {
-  g16_small_cta<EPI, STAGES>(&tmap_a, &tmap_b, args, static_cast<int>(blockIdx.x));
+  g16_small_cta<EPI, STAGES, LONG>(&tmap_a, &tmap_b, args, static_cast<int>(blockIdx.x));
 }
 
 // Two independent products of plain epilogue in one launch, the first's CTAs
@@ -1010,7 +1130,7 @@ __global__ void __launch_bounds__(s16_threads(1), STAGES <= 3 ? 2 : 1)
                    const __grid_constant__ G16Two two) {
   const int cta = static_cast<int>(blockIdx.x);
   const bool second = cta >= two.first_ctas;
-  g16_small_cta<kEpiPlain, STAGES>(second ? &a2 : &a1, second ? &b2 : &b1, second ? two.second : two.first,
+  g16_small_cta<kEpiPlain, STAGES, false>(second ? &a2 : &a1, second ? &b2 : &b1, second ? two.second : two.first,
                                    second ? cta - two.first_ctas : cta);
 }
 
@@ -1127,11 +1247,11 @@ static int64_t lone_clusters(int splits, int num_sms) {
   int v = known[dev][splits].load(std::memory_order_relaxed);
   if (v == 0) {
     static std::atomic<bool> done[kMaxDevices];
-    if (allow_smem(g16_small_kernel<kEpiPlain, 6>, S16Layout<6>::ALLOC, done) != cudaSuccess) return 0;
+    if (allow_smem(g16_small_kernel<kEpiPlain, 6, false>, S16Layout<6>::ALLOC, done) != cudaSuccess) return 0;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = g16_config(splits, s16_threads(splits), S16Layout<6>::ALLOC, splits, nullptr, attr);
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&v, g16_small_kernel<kEpiPlain, 6>, &cfg) != cudaSuccess || v <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&v, g16_small_kernel<kEpiPlain, 6, false>, &cfg) != cudaSuccess || v <= 0) {
       cudaGetLastError();
       v = num_sms / splits / 2;
     }
@@ -1140,23 +1260,31 @@ static int64_t lone_clusters(int splits, int num_sms) {
   return v;
 }
 
-template <int EPI, int STAGES>
+template <int EPI, int STAGES, bool LONG>
 static cudaError_t launch_small16s(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
                                    cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow_smem(g16_small_kernel<EPI, STAGES>, S16Layout<STAGES>::ALLOC, done);
+  cudaError_t e = allow_smem(g16_small_kernel<EPI, STAGES, LONG>, S16Layout<STAGES>::ALLOC, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg =
       g16_config(tiles * a.splits, s16_threads(a.splits), S16Layout<STAGES>::ALLOC, a.splits, stream, attr);
-  return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI, STAGES>, ta, tb, a);
+  return cudaLaunchKernelEx(&cfg, g16_small_kernel<EPI, STAGES, LONG>, ta, tb, a);
+}
+
+// Is a CTA's share of the sum too long for one accumulator?
+static bool small_long(int64_t k, int splits) {
+  const int64_t chunks = (k + kS16K - 1) / kS16K;
+  return (chunks + splits - 1) / splits > kSumWhole / kS16K;
 }
 
 template <int EPI>
 static cudaError_t launch_small16(const CUtensorMap& ta, const CUtensorMap& tb, const G16Args& a, int64_t tiles,
                                   int num_sms, cudaStream_t stream) {
-  return tiles <= lone_clusters(a.splits, num_sms) ? launch_small16s<EPI, 6>(ta, tb, a, tiles, stream)
-                                                   : launch_small16s<EPI, 3>(ta, tb, a, tiles, stream);
+  const bool lone = tiles <= lone_clusters(a.splits, num_sms);
+  if (small_long(a.k, a.splits))
+    return lone ? launch_small16s<EPI, 6, true>(ta, tb, a, tiles, stream) : launch_small16s<EPI, 3, true>(ta, tb, a, tiles, stream);
+  return lone ? launch_small16s<EPI, 6, false>(ta, tb, a, tiles, stream) : launch_small16s<EPI, 3, false>(ta, tb, a, tiles, stream);
 }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1300,6 +1428,7 @@ static cudaError_t prepare16(const Gemm16& p, const G16Choice& c, G16Args* args,
   a.b_per_group = p.mode != kRaggedK;
   a.op_fp16 = p.op_fp16;
   a.out_type = p.out_type;
+  a.epi = p.epi;
   a.act = p.act;
   a.sym = p.sym;
   a.splits = c.splits;
@@ -1335,6 +1464,8 @@ cudaError_t launch_gemm16(const Gemm16& p, int num_sms, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   if (p.res && !make_tmap_out16(&tr, const_cast<void*>(p.res), p.n, p.m, p.groups, p.res_ld, p.res_batch, false))
     return cudaErrorInvalidValue;
+  // (ragged K: one group may have all rows)
+  if (p.out_type != 2 && p.k > kSumWhole) return launch_pair16<kEpiLong>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   if (p.out_type == 2) return launch_pair16<kEpiSum>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   if (p.epi == kEpiLinear) return launch_pair16<kEpiLinear>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
   if (p.epi == kEpiPoly) return launch_pair16<kEpiPoly>(ta, tb, td, tz, tr, a, tiles, num_sms, stream);
@@ -1351,7 +1482,8 @@ cudaError_t launch_gemm16_two(const Gemm16& p, const Gemm16& q, int num_sms, cud
   const int64_t longest = tp.chunks > tq.chunks ? tp.chunks : tq.chunks, fewest = tp.chunks < tq.chunks ? tp.chunks : tq.chunks;
   const bool together = p.mode == kBatched && q.mode == kBatched && p.epi == kEpiPlain && q.epi == kEpiPlain && small_can(p) &&
                         small_can(q) && forced_config() < 0 &&
-                        small_cost(tp.small + tq.small, longest, fewest, epilogue_cost(p), num_sms, &s) < apart;
+                        small_cost(tp.small + tq.small, longest, fewest, epilogue_cost(p), num_sms, &s) < apart &&
+                        !small_long(p.k, s) && !small_long(q.k, s);
   if (!together) {
     const cudaError_t e = launch_gemm16(p, num_sms, stream);
     return e != cudaSuccess ? e : launch_gemm16(q, num_sms, stream);

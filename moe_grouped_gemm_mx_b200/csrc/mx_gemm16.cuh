@@ -28,8 +28,17 @@ enum G16Mode : int { kBatched = 0, kRaggedM = 1, kRaggedK = 2 };
 // kEpiPlain: D = acc.  kEpiLinear: z = acc + bias, D = act(z) + residual.
 // kEpiPoly: D = alpha * scale * acc + beta * (C + C_lo) + diag * I, with an
 // optional low half of D and, for a symmetric D, the mirrored tile.
-// kEpiSum: D = acc in FP32 (pair kernel only).
-enum G16Epi : int { kEpiPlain = 0, kEpiLinear = 1, kEpiPoly = 2, kEpiSum = 3 };
+// Of the pair kernel only: kEpiSum: D = acc in FP32.  kEpiLong: one of the first three
+// (args.epi) behind a long sum.
+enum G16Epi : int { kEpiPlain = 0, kEpiLinear = 1, kEpiPoly = 2, kEpiSum = 3, kEpiLong = 4 };
+
+// The tensor core's accumulator truncates: a sum of numbers of one sign loses
+// about 1e-7 of itself for each 16 terms (6.2e-3 at 2^20 of them, more than half a
+// step of BF16).  One accumulator therefore takes at most kSumWhole terms (1e-4, a
+// fifth of FP16's half step); a longer sum goes in parts of kSumPart, which are
+// added in FP32, rounded (5e-5 whatever its length).
+constexpr int kSumWhole = 1 << 14;
+constexpr int kSumPart = 1 << 13;
 
 struct G16Args {
   const void* bias;              // [n], operand type (linear)
@@ -54,6 +63,7 @@ struct G16Args {
   int b_per_group;               // B has a z coordinate (batched, ragged M)
   int op_fp16;                   // operands are FP16 (else BF16); also the type of bias, residual, C
   int out_type;                  // MX_BF16 / MX_FP16 / MX_FP32 of D and z
+  int epi;                       // kEpiPlain, kEpiLinear or kEpiPoly
   int act;
   int sym;                       // D is symmetric: only tiles on and above the diagonal are computed
   int splits;                    // one-CTA kernel: CTAs of a cluster that share one tile's K
@@ -246,11 +256,27 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
       : "memory");
 }
 
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Bounded wait for a phase of a barrier, with the meaning of mbar_wait.  The
-// clock is read only once 32 attempts have failed: reading it after the first,
+// clock is read only once TRIES attempts have failed: reading it after the first,
 // as mbar_wait does, delays every wait of a pipeline in step (the producer's for
-// a free stage, the MMA issuer's for a full one) by that read.
-template <bool CLUSTER>
+// a free stage, the MMA issuer's for a full one) by that read (after two: 512 rows
+// over 32 experts 0.8 % slower).  An attempt that fails takes up to 4 us, so 32 keep a
+// limit to within some 250 us; 2, for waits outside the pipeline, to 16.
+template <bool CLUSTER, uint32_t TRIES = 32>
 __device__ __forceinline__ bool wait16(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
@@ -266,7 +292,7 @@ __device__ __forceinline__ bool wait16(uint32_t bar, uint32_t parity, volatile i
     else
       ok = mbar_try_wait(bar, parity);
     if (ok) return true;
-    if ((it & 31u) == 0) {
+    if (it % TRIES == 0) {
       if (abort != nullptr && *abort) return false;
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
