@@ -553,7 +553,8 @@ mx_status mx_grouped_gemm_ragged_wgrad(const void *dd, const void *a, const int3
  *   A = X X^T;  X = a X + (b A + c A^2) X        (X^T X for more rows than columns)
  *   g [batch, m, n], MX_BF16 or MX_FP32 (g_dtype); out [batch, m, n] BF16; coeffs
  *   a HOST array of 3 * steps floats, read during the call.
- * Products are of FP16 numbers scaled by powers of two, with FP32 sums.  The
+ * Products are of FP16 numbers scaled by powers of two, with FP32 sums, also where
+ * eps is much larger than G.  The
  * coefficients must keep the singular values, which start in [0, 1], at most
  * 3.9, and |b s^2 + c s^4| and |a + b s^2 + c s^4| at most 15.5 on the way (FP16's
  * range; the usual (3.4445, -4.775, 2.0315) stays below 1.3 and 3.5), else

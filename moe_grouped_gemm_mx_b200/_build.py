@@ -23,7 +23,8 @@ LIB = os.path.join(HERE, "libmx.so")
 SOURCES = ["mx_api.cu", "mx_gemm.cu", "mx_gemm2.cu", "mx_quant.cu", "mx_quant_t.cu", "mx_quant_tw.cu",
            "mx_gemm_tw.cu", "mx_moe.cu", "mx_gemm16.cu", "mx_act.cu", "mx_ortho.cu",
            "mx_ortho_small.cu"]
-HEADERS = ["mx_ptx.cuh", "mx_launch.h", "mx_fastdiv.h", "mx_gemm_common.cuh", "mx_mxfp8.cuh", "mx_gemm16.cuh"]
+HEADERS = ["mx_ptx.cuh", "mx_launch.h", "mx_fastdiv.h", "mx_gemm_common.cuh", "mx_mxfp8.cuh", "mx_gemm16.cuh",
+           "mx_ortho.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -12,12 +12,16 @@
 // about sqrt(columns); A and B times 2^12), so that FP16's range is not left and
 // its 11 bits are kept.  An iteration multiplies the smallest singular values by
 // about a = 3.4, and so the rounding of X in those directions: five steps
-// multiply the first rounding by nearly 500.  Therefore X_0 is not rounded at
-// all for a 16-bit G (G times a power of two; the rest of 1 / |G|_F is a factor
+// multiply the first rounding by nearly 500.  Therefore X_0 of a 16-bit G is G
+// times a power of two, exact but for entries below some 2^-14 of the norm over the root of
+// the columns, which fall below FP16's normal range (the rest of 1 / |G|_F is a factor
 // of the first step's epilogues), and X is kept as the sum of two FP16 numbers
 // while three or more steps follow, the low one entering a X in the
 // epilogue.  The products take the high one: B maps into the directions of the
 // large singular values, where its rounding is not multiplied.  A, B: one FP16 number.
+// While X is small as a whole (eps much larger than G: X_0's norm is |G| / eps) it is held
+// times a power of two more, one for each matrix and step, found from a bound of its
+// singular values; the epilogues' factors on the device bring them in and out.
 //
 // Bound by the tensor cores: five steps of 8 x 4096 x 7168 are 17.2 TFLOP and take
 // 12.9 ms on a card that has rested (1330 TFLOP/s), 15.3 in loops at its power limit,
@@ -33,11 +37,11 @@
 
 #include "mx_gemm16.cuh"
 #include "mx_launch.h"
+#include "mx_ortho.cuh"
 
 namespace mxk {
 
 constexpr int kNormParts = 256; // partial sums of squares per matrix
-constexpr int kLogSA = 12;      // A and B are held times 2^12
 
 // Sum of squares of a share of each matrix, in 64 bits: no square of an FP32
 // or BF16 number over- or underflows there.
@@ -84,12 +88,23 @@ __global__ void __launch_bounds__(256) ns_square_kernel(const T* __restrict__ g,
   }
 }
 
-// X_0 = G 2^(sx - e) as FP16 (and, for an FP32 G, what that leaves), rows
-// `pitch` apart; scale = 2^e / (|G|_F + eps), in (1/2, 1].  One warp a row.
+struct NsCoeffs {
+  float v[3 * kNsMaxSteps];
+  int steps;
+};
+
+// X_0 = G 2^(sx - e) as FP16 (and, for an FP32 G, what that leaves), 2^e at most |G|_F, rows
+// `pitch` apart.  One warp a row.  And the factors of each step's epilogues,
+// [step][matrix]: before step i > 0 what is stored is X 2^(sx - f_i), f_i = 0 unless
+// X is small; before the first it is X 2^sx (|G|_F + eps) / 2^e.
+//   gram: what XX^T's X still has to be multiplied by, 2^e / (|G|_F + eps), later 2^f_i
+//   next: gram / 2^f_(i+1), f = 0 behind the last step
+// (both are 2^e / (|G|_F + eps), later 1, for a matrix much larger than eps)
 template <typename T>
 __global__ void __launch_bounds__(256) ns_start_kernel(const T* __restrict__ g, const double* __restrict__ part, int parts,
                                                        float eps, int log_sx, __half* __restrict__ hi, __half* __restrict__ lo,
-                                                       float* __restrict__ scale, int64_t m, int n, int64_t pitch) {
+                                                       float* __restrict__ gram, float* __restrict__ next,
+                                                       const __grid_constant__ NsCoeffs coeffs, int64_t m, int n, int64_t pitch) {
   __shared__ int exponent;
   pdl_launch_dependents();
   pdl_wait_prior();
@@ -98,13 +113,22 @@ __global__ void __launch_bounds__(256) ns_start_kernel(const T* __restrict__ g, 
     double s = 0.0;
     for (int i = lane; i < parts; i += 32) s += part[blockIdx.y * kNormParts + i];
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const double f = sqrt(s) + static_cast<double>(eps);
-    const bool usual = f > 0.0 && isfinite(f);  // else zero (eps = 0) or not finite: every entry becomes NaN or 0 below
-    const int e = usual ? ilogb(f) : 0;
+    const double norm = sqrt(s), f = norm + static_cast<double>(eps);
+    const bool usual = norm > 0.0 && isfinite(norm);  // else zeros stay zeros, and what is not finite makes all NaN
+    const int e = usual ? ilogb(norm) : 0;
     if (lane == 0) {
       exponent = e;
-      if (blockIdx.x == 0)
-        scale[blockIdx.y] = usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("");
+      if (blockIdx.x == 0) {
+        double have = usual ? scalbn(1.0, e) / f : norm == 0.0 ? 1.0 : nan("");
+        float bound = usual ? static_cast<float>(norm / f) : 1.0f;
+        for (int i = 0; i < coeffs.steps; ++i) {
+          bound = ns_next_bound(bound, coeffs.v + 3 * i);
+          const int up = bound < kNsSmall && i + 1 < coeffs.steps ? (bound > 0x1p-120f ? ilogbf(bound) : -120) : 0;
+          gram[static_cast<int64_t>(i) * gridDim.y + blockIdx.y] = static_cast<float>(have);
+          next[static_cast<int64_t>(i) * gridDim.y + blockIdx.y] = static_cast<float>(scalbn(have, -up));
+          have = scalbn(1.0, up);
+        }
+      }
     }
   }
   __syncthreads();
@@ -169,7 +193,7 @@ static size_t pad256(size_t v) { return (v + 255) / 256 * 256; }
 struct NsPlan {
   int64_t pitch_x, pitch_a, count_x, count_a;  // elements
   bool low;                                    // the low halves of X are kept
-  size_t part, scale, x[2], xl[2], a, b, bytes;
+  size_t part, gram, next, x[2], xl[2], a, b, bytes;
 };
 
 static NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, bool fp32, int steps) {
@@ -187,7 +211,8 @@ static NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, bool fp32, int steps)
     return here;
   };
   p.part = take(static_cast<size_t>(batch) * kNormParts * 8);
-  p.scale = take(static_cast<size_t>(batch) * 4);
+  p.gram = take(static_cast<size_t>(batch) * steps * 4);
+  p.next = take(static_cast<size_t>(batch) * steps * 4);
   for (int i = 0; i < 2; ++i) {
     p.x[i] = take(static_cast<size_t>(batch * p.count_x) * 2);
     p.xl[i] = p.low ? take(static_cast<size_t>(batch * p.count_x) * 2) : 0;
@@ -226,11 +251,15 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
   const NsPlan p = ns_plan(q.batch, q.m, q.n, q.fp32, q.steps);
   uint8_t* ws = static_cast<uint8_t*>(q.workspace);
   double* part = reinterpret_cast<double*>(ws + p.part);
-  float* scale = reinterpret_cast<float*>(ws + p.scale);
+  float* gram = reinterpret_cast<float*>(ws + p.gram);
+  float* next = reinterpret_cast<float*>(ws + p.next);
+  NsCoeffs coeffs = {};
+  coeffs.steps = q.steps;
+  for (int i = 0; i < 3 * q.steps; ++i) coeffs.v[i] = q.coeffs[i];
   const bool tall = q.m > q.n;
   const int64_t r = tall ? q.n : q.m, c = tall ? q.m : q.n;
   const int log_sx = static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(c))));
-  const float sx = std::ldexp(1.0f, log_sx), sa = std::ldexp(1.0f, kLogSA);
+  const float sx = std::ldexp(1.0f, log_sx), sa = std::ldexp(1.0f, kNsLogSA);
 
   // enough blocks for the GPU over the whole batch, none without work
   const int64_t count = q.m * q.n;
@@ -250,13 +279,13 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
     e = launch_pdl(ns_square_kernel<float>, grid_sq, stream, g, part, count);
     if (e != cudaSuccess) return e;
     e = launch_pdl(ns_start_kernel<float>, grid_st, stream, g, static_cast<const double*>(part), static_cast<int>(parts),
-                   q.eps, log_sx, x0, x0l, scale, q.m, static_cast<int>(q.n), p.pitch_x);
+                   q.eps, log_sx, x0, x0l, gram, next, coeffs, q.m, static_cast<int>(q.n), p.pitch_x);
   } else {
     const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(q.g);
     e = launch_pdl(ns_square_kernel<__nv_bfloat16>, grid_sq, stream, g, part, count);
     if (e != cudaSuccess) return e;
     e = launch_pdl(ns_start_kernel<__nv_bfloat16>, grid_st, stream, g, static_cast<const double*>(part),
-                   static_cast<int>(parts), q.eps, log_sx, x0, x0l, scale, q.m, static_cast<int>(q.n), p.pitch_x);
+                   static_cast<int>(parts), q.eps, log_sx, x0, x0l, gram, next, coeffs, q.m, static_cast<int>(q.n), p.pitch_x);
   }
   if (e != cudaSuccess) return e;
 
@@ -277,7 +306,7 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
     s.epi = 2;
     s.status = q.status;
 
-    // A 2^12 = X X^T 2^(12 - 2 sx) scale^2
+    // A 2^12 = X X^T 2^(12 - 2 sx) gram^2
     Gemm16 ga = s;
     ga.a = ga.b = x;
     ga.a_ld = ga.b_ld = p.pitch_x;
@@ -290,7 +319,7 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
     ga.d_batch = p.count_a;
     ga.sym = 1;
     ga.alpha = sa / (sx * sx);
-    ga.scale = i == 0 ? scale : nullptr;
+    ga.scale = gram + i * q.batch;
     ga.scale_pow = 2;
     e = launch_gemm16(ga, num_sms, stream);
     if (e != cudaSuccess) return e;
@@ -314,7 +343,7 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
     e = launch_gemm16(gb, num_sms, stream);
     if (e != cudaSuccess) return e;
 
-    // X 2^sx = a (X 2^sx) + 2^-12 (B 2^12) (X 2^sx); the last one without 2^sx, to the output
+    // X 2^sx = (a (X 2^sx) + 2^-12 (B 2^12) (X 2^sx)) next; the last one without 2^sx, to the output
     Gemm16 gx = s;
     if (tall) {  // X B, B symmetric
       gx.a = x;
@@ -337,7 +366,7 @@ cudaError_t launch_orthogonalize(const OrthoProblem& q, int num_sms, cudaStream_
     gx.k = r;
     const float unit = last ? 1.0f / sx : 1.0f;
     gx.alpha = unit / sa;
-    gx.scale = i == 0 ? scale : nullptr;
+    gx.scale = next + i * q.batch;
     gx.scale_pow = 1;
     if (add_x) {
       gx.res = x;

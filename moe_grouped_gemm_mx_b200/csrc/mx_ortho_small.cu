@@ -33,14 +33,13 @@
 
 #include "mx_gemm16.cuh"
 #include "mx_launch.h"
+#include "mx_ortho.cuh"
 
 namespace mxk {
 
-constexpr int kNsMaxSteps = 16;
 constexpr int kNsThreads = 512;  // four warps per TMEM lane quarter
 constexpr int kNsGroups = kNsThreads / 128;
 constexpr int kNsSmem = 232448;
-constexpr int kNsLogSA = 12;     // A and B are held times 2^12
 constexpr int kNsMaxCluster = 16;
 
 struct NsSmallArgs {
@@ -52,6 +51,7 @@ struct NsSmallArgs {
   int slice;        // columns of the long side per CTA, a multiple of 64
   int steps;
   int log_sx;
+  uint32_t keep;    // steps (a bit each) that take a X of the FP32 X for a matrix much larger than eps
   float eps;
   float coeffs[3 * kNsMaxSteps];
 };
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const uint32_t as = xs + chunks * rp * 128;                        // A
   const uint32_t bs = as + (rp + 63) / 64 * rp * 128;                // B
   const uint32_t recv = bs + (rp + 63) / 64 * rp * 128;              // [source][column][row] partial sums
-  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8, factors 3 x 4, failed 4, drain barrier 8
+  // misc: barrier 8, TMEM address 4, pad 4, block sums 16 x 8, cluster sums 16 x 8, factors 3 x 4, failed 4, drain barrier 8, kept steps 4
   const uint32_t bar = misc;
   auto at = [&](uint32_t addr) { return smem + (addr - sbase); };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(at(misc + 8));
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
   const uint32_t cluster_sums = misc + 144;
   volatile float* factors = reinterpret_cast<volatile float*>(at(misc + 272));
   const uint32_t failed = misc + 284, drain_bar = misc + 288;
+  volatile uint32_t* kept = reinterpret_cast<volatile uint32_t*>(at(misc + 296));
 
   if (tid == 0) {
     mbar_init(bar, 1);
@@ -267,9 +268,18 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     factors[0] = scalbnf(1.0f, shift / 2);
     factors[1] = scalbnf(1.0f, shift - shift / 2);
     factors[2] = (usual ? static_cast<float>(scalbn(1.0, e) / f) : f == 0.0 ? 1.0f : nanf("")) * (1 << kNsLogSA);
+    uint32_t keep = args.keep;
+    float bound = usual ? static_cast<float>(sqrt(sum) / f) : 1.0f;
+    if (bound < kNsSmall)  // (a larger one is at most a sixteenth of what `keep` was made for)
+      for (int i = 0; i < args.steps; ++i) {
+        if (bound < kNsSmall) keep |= 1u << i;
+        bound = ns_next_bound(bound, args.coeffs + 3 * i);
+      }
+    *kept = keep;
   }
   __syncthreads();
   const float up0 = factors[0], up1 = factors[1], up2 = factors[2];
+  const uint32_t keep = *kept;
   const float sa = static_cast<float>(1 << kNsLogSA), inv_sa = 1.0f / sa;
 
   // FP16 copy of a chunk of X for the products (rows of zeros up to rp); v: X 2^(sx + 12)
@@ -333,8 +343,9 @@ __global__ void __launch_bounds__(kNsThreads, 1) ns_cluster_kernel(const __grid_
     __syncwarp();
     // ---- meanwhile a X in TMEM.  The last two steps take (a I + B) X of the FP16 X
     // instead, as the general form does: nothing multiplies X's rounding any more,
-    // and a X of one X with B X of another would only add the difference.
-    const bool add_x = step == 0 || step + 2 < args.steps;
+    // and a X of one X with B X of another would only add the difference (but not while
+    // X is small, when a X is all that counts and FP16 has few bits of it).
+    const bool add_x = keep >> step & 1;
     for (int j = add_x && ok ? first : chunks; j < chunks; j += kNsGroups) {
       uint32_t v[2][32];
       load_x(j, v[0], v[1]);
@@ -612,6 +623,11 @@ static cudaError_t ns_small(const OrthoProblem& q, bool* taken, int num_sms, cud
   a.log_sx = static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(c))));
   a.eps = q.eps;
   for (int i = 0; i < 3 * q.steps; ++i) a.coeffs[i] = q.coeffs[i];
+  float bound = 1.0f;
+  for (int i = 0; i < q.steps; ++i) {
+    if (i == 0 || i + 2 < q.steps || bound < kNsSmall) a.keep |= 1u << i;
+    bound = ns_next_bound(bound, q.coeffs + 3 * i);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(static_cast<unsigned>(q.batch * cs), 1, 1);
