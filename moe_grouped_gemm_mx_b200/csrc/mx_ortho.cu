@@ -211,8 +211,8 @@ static NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, bool fp32, int steps)
     return here;
   };
   p.part = take(static_cast<size_t>(batch) * kNormParts * 8);
-  p.gram = take(static_cast<size_t>(batch) * steps * 4);
-  p.next = take(static_cast<size_t>(batch) * steps * 4);
+  p.gram = take(static_cast<size_t>(batch) * kNsMaxSteps * 4);  // (for any number of steps: a workspace serves them alike)
+  p.next = take(static_cast<size_t>(batch) * kNsMaxSteps * 4);
   for (int i = 0; i < 2; ++i) {
     p.x[i] = take(static_cast<size_t>(batch * p.count_x) * 2);
     p.xl[i] = p.low ? take(static_cast<size_t>(batch * p.count_x) * 2) : 0;

@@ -109,3 +109,11 @@ def test_orthogonalize(lib):
     assert f(g=FAKE + 8) == f(out=FAKE + 8) == f(work=FAKE + 16) == MX_ERR_MISALIGNED
     assert f(g=None, out=None, work=None, batch=0) == f(g=None, out=None, work=None, m=0) == MX_OK
     assert lib.mx_orthogonalize(FAKE, BF16, FAKE, 1, 8, 8, 5, None, 1e-7, FAKE, 1 << 30, None, None) == MX_ERR_INVALID_ARGUMENT
+
+
+def test_orthogonalize_workspace_serves_other_step_counts(lib):
+    """From four steps on (fewer may do with less) the number of steps does not change the size."""
+    ws = lib.mx_orthogonalize_workspace_bytes
+    for batch, m, n in ((1, 1, 1), (3, 129, 257), (70, 300, 200)):
+        assert len({ws(batch, m, n, BF16, steps) for steps in range(4, 17)}) == 1
+        assert len({ws(batch, m, n, FP32, steps) for steps in range(1, 17)}) == 1
