@@ -124,6 +124,30 @@ def test_ragged_weight_gradient(mx, dtype, out_dtype):
     assert intact()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_ragged_weight_gradient_in_32_bits(mx, dtype):
+    """FP32 results add a part of 512 rows at a time: (512 / 16 + 16) 2^-22 of the sum for the
+    parts, 2^-24 for each addition and the last rounding.  (One accumulator would lose 3e-5
+    of 5003 rows, three times that.)  More tiles than CTA pairs, sums of one part and of
+    many, ends inside a step of 16 in the first part and in later ones."""
+    counts = [511, 512, 513, 0, 1024, 1025, 3, 5003, 2 ** 16 + 3, 1536]
+    n, k = 1288, 1032
+    first, rows = 5, 5 + sum(counts) + 4
+    off = torch.tensor([first + sum(counts[:i]) for i in range(len(counts) + 1)], dtype=torch.int32, device="cuda")
+    dd, a = positive((rows, n), dtype, 3, 0.125), positive((rows, k), dtype, 4)
+    for t in (dd, a):
+        t[:first] = float("nan")
+        t[-4:] = float("inf")
+    db, intact = guarded((len(counts), n, k), FP32)
+    mx.mx_grouped_gemm_ragged_wgrad(dd, a, off, db=db)
+    for e, c in enumerate(counts):
+        at = first + sum(counts[:e])
+        ref = dd[at:at + c].double().T @ a[at:at + c].double()
+        tol = (512 / 16 + 16) * 2.0 ** -22 + (-(-c // 512) + 1) * 2.0 ** -24
+        close(db[e], ref, tol * ref.abs(), f"expert {e} of {c} rows")
+    assert intact()
+
+
 def test_several_tiles_a_pair(mx):
     """More 256 x 256 tiles than CTA pairs: sums of one part and of several take turns in a pair's accumulators."""
     counts = [20000, 0, 300, 17001, 16384, 9000, 40003]
