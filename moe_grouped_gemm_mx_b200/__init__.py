@@ -830,6 +830,12 @@ def _operand16(t: torch.Tensor, name: str, dims: int) -> torch.dtype:
     return dt
 
 
+def _workspace16(t: torch.Tensor, device):
+    """A contiguous byte tensor of any size on the given device (the library checks its size)."""
+    _check(t, torch.uint8, "workspace")
+    _check16(t, "workspace", (t.numel(),), torch.uint8, device)
+
+
 def _status_on(dev_status, device):
     if dev_status is None:
         return None
@@ -930,7 +936,7 @@ def mx_linear_act_backward(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Te
     if dz is not None:
         _check16(dz, "dz", (m, n), dt, dev)
     if workspace is not None:
-        _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+        _workspace16(workspace, dev)
     s, contexts = _begin(dy, stream)
     try:
         if w is not None and dx is None:
@@ -1029,7 +1035,8 @@ def mx_grouped_gemm_ragged_wgrad(dd: torch.Tensor, a: torch.Tensor, group_offset
         raise ValueError("group_offsets must be a 1-D tensor of groups + 1 entries")
     groups = group_offsets.numel() - 1
     _offsets(group_offsets, groups, dev)
-    out_dtype = (dt if db is None else db.dtype) if out_dtype is None else out_dtype
+    if out_dtype is None:
+        out_dtype = db.dtype if isinstance(db, torch.Tensor) else dt
     if out_dtype not in (dt, torch.float32):
         raise TypeError(f"out_dtype must be {dt} or torch.float32, got {out_dtype}")
     s, contexts = _begin(dd, stream)
@@ -1090,7 +1097,7 @@ def mx_orthogonalize(g: torch.Tensor, steps: int = 5, coeffs=(3.4445, -4.7750, 2
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
-            _check16(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+            _workspace16(workspace, dev)
         _raise(_lib.mx_orthogonalize(_ptr(g), _DTYPES[g.dtype], _ptr(out), batch, m, n, steps,
                                      (ctypes.c_float * len(flat))(*flat), eps, _ptr(workspace), workspace.numel(),
                                      _status_on(dev_status, dev), s), "mx_orthogonalize")
