@@ -479,7 +479,7 @@ mx_status mx_moe_combine_peer(const void *const *y_peers, int32_t ranks, int64_t
 typedef enum mx_dtype { MX_BF16 = 0, MX_FP16 = 1, MX_FP32 = 2 } mx_dtype;
 
 /* act(z): z; max(z, 0); z / (1 + e^-z); z Phi(z) (Phi the normal distribution
- * function); z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+ * function, within 1.5e-7); z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
 typedef enum mx_activation {
     MX_ACT_NONE = 0,
     MX_ACT_RELU = 1,
@@ -506,9 +506,9 @@ mx_status mx_linear_act(const void *x, const void *w, const void *bias, const vo
  * Its backward pass, from dy = dL/dy [m, n] and the z that the forward pass kept:
  *   dz = dy * act'(z);   dx = dz w;   dw = dz^T x;   dbias[j] = sum_i dz[i, j]
  * (the residual's gradient is dy).  dx [m, k], dw [n, k] and dbias [n] are each
- * nullable: not wanted.  With an activation, z and dz [m, n] (out; rounded to
- * `dtype` for the two products) are needed; without one both may be NULL and dy
- * takes dz's place.  dbias sums the unrounded products in FP32 in a fixed order;
+ * nullable: not wanted (none wanted: a no-op, dz is not written either).  With an
+ * activation, z and dz [m, n] (out; rounded to `dtype` for the two products) are
+ * needed; without one both may be NULL and dy takes dz's place.  dbias sums the unrounded products in FP32 in a fixed order;
  * it needs `workspace` of mx_linear_act_backward_workspace_bytes(m, n) bytes (none
  * up to m = 1024).
  * ReLU's derivative at zero is 0.  x is read for dw only, w for dx only (NULL

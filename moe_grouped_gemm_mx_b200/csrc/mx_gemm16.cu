@@ -13,6 +13,8 @@
 //                  (linear and poly: warps 2-17, four per quarter, 64 columns each)
 //      warp 10     ragged K only (both CTAs): clears the rows of the stage that
 //                  lie behind the group's last token before the MMAs read them
+//    (Times here and below: captured graphs on a card that has rested.  A call outside a
+//    graph adds the host's part to small ones, loops of seconds the power limit to large ones.)
 //    Bound by the tensor cores: 8192x4096x4096 in 178 us (1550 TFLOP/s; in loops of
 //    seconds the card's power holds it to 1310, as it does the library product);
 //    with GELU and the pre-activation the tensor pipe is active 82 % of the time.
@@ -28,7 +30,7 @@
 //    fixed order), two CTAs to an SM.  For products that would leave most SMs
 //    idle in 256 x 256 tiles, where the operands' bytes bound the time: 512 rows
 //    over 32 experts of 4096x7168 read 1.88 GB in 305 us, 6170 GB/s, what a copy of as
-//    many bytes takes.  The smallest are bound by latency: of a lone 128x128x64
+//    many bytes takes (called with inputs not in L2: 344 us, 5480).  The smallest are bound by latency: of a lone 128x128x64
 //    tile's 3.8 us (plain) 2.1 are the launch's and 1.0 the operands' and the MMAs';
 //    64x2112x7168 by 4 takes 12.6 us, its bytes 4.8.
 #include <cuda.h>
@@ -721,6 +723,8 @@ __global__ void __launch_bounds__(p16_threads(EPI), 1)
 // CTA finishes a quarter or less.
 __host__ __device__ constexpr int s16_threads(int splits) { return splits <= 2 ? 320 : 192; }
 constexpr int kS16T = 128;        // tile rows and columns
+// (With three stages, and so 96 registers, the linear epilogue spills 8 bytes and the poly one
+// 64, LONG ones 84 to 260; of the pair kernel poly spills 16, kEpiLong 270.)
 constexpr int kS16K = 64;
 
 // STAGES: 3 where two CTAs share an SM, 6 where a CTA has one to itself (the
@@ -747,8 +751,7 @@ struct S16Layout {
 
 // One CTA's part of a product: `cta` counts from the product's first CTA.  LONG: its
 // sum goes through the accumulator in parts of kSumPart, which the epilogue's warps
-// add up in TMEM columns behind it (64x2112x65536: 2 % of the time).  With three stages,
-// and so 96 registers, it spills 84 to 260 bytes, outside the loop over K.
+// add up in TMEM columns behind it (64x2112x65536: 2 % of the time).
 template <int EPI, int STAGES, bool LONG>
 __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const CUtensorMap* tmap_b, const G16Args& args,
                                               const int cta) {
@@ -772,7 +775,7 @@ __device__ __forceinline__ void g16_small_cta(const CUtensorMap* tmap_a, const C
   auto empty_bar = [&](int s) { return sbase + L::OFF_BAR + 8u * (S + s); };
   const uint32_t acc_bar = sbase + L::OFF_BAR + 8u * (2 * S);
   const uint32_t added_bar = acc_bar + 8, drain_bar = acc_bar + 16;  // LONG
-  constexpr int kTmem = LONG ? 2 * kS16T : kS16T;
+  constexpr int kTmem = LONG ? 2 * kS16T : kS16T;  // of two CTAs to an SM: no more than TMEM's 512, so neither waits
   constexpr int kPart = kSumPart / kS16K;  // chunks of an accumulator
 
   if (threadIdx.x == 0) {
