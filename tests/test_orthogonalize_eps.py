@@ -104,3 +104,20 @@ def test_every_kernel(mx, cfg, monkeypatch):
     monkeypatch.setenv("MX_GEMM16_CONFIG", cfg)
     for dtype in (BF16, FP32):
         check(mx, batch_of((264, 520), dtype, 1.0, RATIOS, 4), [COEFFS] * 5, 1.0)
+
+
+@pytest.mark.parametrize("form", ["", "general"])
+def test_no_linear_term(mx, form, monkeypatch):
+    """a = 0: a small X falls with its cube, past what the products can resolve.  The result stays
+    finite; where it is large, each step triples an error and adds three FP16 roundings
+    of its own (13 times 3 times 2^-11 in three steps), where it is small, FP16's smallest steps
+    in A and B, held times 2^12, leave less than 1e-7 of X a step."""
+    monkeypatch.setenv("MX_ORTHO_CONFIG", form)
+    coeffs = [(0.0, 1.0, 0.0)] * 3
+    g = batch_of((72, 136), BF16, 1.0, RATIOS, 5)
+    got = mx.mx_orthogonalize(g, steps=3, coeffs=coeffs, eps=1.0).double()
+    assert bool(torch.isfinite(got).all())
+    for i, r in enumerate(RATIOS):
+        ref = exact(g[i], coeffs, 1.0)
+        off = float(torch.linalg.vector_norm(got[i] - ref))
+        assert off <= (2.0 ** -8 + 39 * 2.0 ** -11) * float(torch.linalg.vector_norm(ref)) + 3e-7 * r, (r, off)
