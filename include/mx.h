@@ -581,7 +581,8 @@ mx_status mx_orthogonalize(const void *g, int32_t g_dtype, void *out_bf16, int64
  * in nanoseconds, for the GEMM launches that follow, from any thread
  * (ns == 0 restores the default); a limit below a kernel's legitimate waits
  * makes its calls fail with MX_DEV_TIMEOUT, which is how the failure path is
- * tested.  Never fails. */
+ * tested.  A kernel looks at the clock now and then: a wait may last some 250 us
+ * longer than the limit.  Never fails. */
 mx_status mx_set_wait_limit_ns(uint64_t ns);
 /* The current limit in nanoseconds. */
 uint64_t mx_wait_limit_ns(void);
